@@ -1,0 +1,509 @@
+// Device helpers of the attention kernels: visibility of keys, LDS tiles and
+// matrix-core fragments.
+//
+// Every product runs on v_mfma_f32_32x32x16_bf16.  Lane l of a wave is (l %
+// 32, half l / 32); its 8 values of an A or B operand are k = 8 half .. 8
+// half + 7 of row (column) l % 32, and its 16 results are column l % 32, rows
+// 8 (i / 4) + 4 half + i % 4.  A product whose result is the next product's B
+// operand (P of the scores, dS) stays in registers: the results i = 8 t .. 8 t
+// + 7 are taken as the operand of step t, which makes the contracted index of
+// slot e the row 16 t + 8 (e / 4) + 4 half + e % 4, and the A operand is read
+// from LDS in that order.
+#pragma once
+
+#include "lm_common.hpp"
+
+namespace muon {
+namespace attn {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxPos = 1 << 29;
+
+// Extras of the scores, as template bits.
+constexpr int kCap = 1;
+constexpr int kBias = 2;
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ int lane_id() { return threadIdx.x & 63; }
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// The other half's value of the same column (lane ^ 32).
+__device__ __forceinline__ float other_half(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+__device__ __forceinline__ float half_max(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float half_sum(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Buffer descriptor over `bytes` bytes at p: loads past the end give zero.
+__device__ __forceinline__ auto rsrc(const void* p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00027000);
+}
+
+// LDS tile of kTile rows of DP (head size padded to 64, 96 or 128) bf16.
+// Chunk c (16 bytes) of row r lies at slot c ^ f(r).  f makes 16 consecutive
+// rows of one chunk fall on distinct banks (operands read along the row, 16
+// bytes a lane) and 4 rows of one 64-byte piece too (transposing reads).  The
+// 192-byte rows of DP = 96 are padded to 208 bytes instead.
+template <int DP>
+struct Tile {
+    static constexpr int CPR = DP / 8;
+    static constexpr int LD = DP == 96 ? 104 : DP;
+    static constexpr int ELEMS = kTile * LD;
+    __device__ static __forceinline__ int f(int r) {
+        if constexpr (DP == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
+        else if constexpr (DP == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+        else return 0;
+    }
+    __device__ static __forceinline__ int at(int r, int c) { return r * LD + ((c ^ f(r)) << 3); }
+};
+
+// Moves one tile of kTile rows from memory through registers to LDS.  Rows
+// past `rows` and values past the head size come as zeros, whatever memory
+// holds there.
+template <int DP, int NT>
+struct Loader {
+    static constexpr int N = kTile * Tile<DP>::CPR / NT;
+    static_assert(N * NT == kTile * Tile<DP>::CPR, "whole chunks per thread");
+    uint32_t voff[N];
+    int lds[N];
+    u32x4 reg[N];
+    const bf16_t* base;  // row 0 of the sequence
+    int64_t stride;      // elements per row
+    int rows;
+    uint32_t row_bytes;
+
+    __device__ __forceinline__ void init(const bf16_t* p, int64_t s, int nrows, int d) {
+        base = p;
+        stride = s;
+        rows = nrows;
+        row_bytes = 2 * d;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int id = static_cast<int>(threadIdx.x) % NT + i * NT;
+            const int r = id / Tile<DP>::CPR, c = id % Tile<DP>::CPR;
+            voff[i] = 8 * c < d ? static_cast<uint32_t>(r) * static_cast<uint32_t>(2 * s) + 16 * c : 0x80000000u;
+            lds[i] = Tile<DP>::at(r, c);
+        }
+    }
+    __device__ __forceinline__ void load(int row0) {
+        const int left = rows - row0 < kTile ? rows - row0 : kTile;
+        const uint32_t bytes = left > 0 ? static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(2 * stride) + row_bytes : 0;
+        const auto r = rsrc(base + static_cast<int64_t>(row0) * stride, bytes);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            reg[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff[i], 0, 0));
+    }
+    __device__ __forceinline__ void store(bf16_t* tile) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<u32x4*>(tile + lds[i]) = reg[i];
+    }
+};
+
+// A operand read along the rows of a tile: rows 32 rb + lane % 32, columns 16
+// t + 8 half .. + 7.
+template <int DP>
+struct RowFrag {
+    int off[DP / 16];
+    __device__ __forceinline__ void init() {
+        const int r = lane_id() & 31, h = lane_id() >> 5;
+#pragma unroll
+        for (int t = 0; t < DP / 16; ++t) off[t] = Tile<DP>::at(r, 2 * t + h);
+    }
+    __device__ __forceinline__ bf16x8 read(const bf16_t* tile, int rb, int t) const {
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(tile + 32 * rb * Tile<DP>::LD + off[t]));
+    }
+};
+
+// A operand read across the rows (the tile's transpose): columns 32 dt + lane
+// % 32, contracted rows 16 t + 8 (e / 4) + 4 half + e % 4 for e = 0 .. 7.
+// ds_read_b64_tr_b16: in every 16 lanes, lane r supplies the address of 4
+// values (k + r / 4, c + 4 (r % 4)) and lane i receives (k .. k + 3, c + i).
+template <int DP>
+struct ColFrag {
+    int off[DP / 32][2];
+    __device__ __forceinline__ void init() {
+        const int g = lane_id() >> 4, r = lane_id() & 15, h = g >> 1;
+#pragma unroll
+        for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * e + 4 * h + (r >> 2);
+                const int col = 32 * dt + 16 * (g & 1) + 4 * (r & 3);
+                off[dt][e] = Tile<DP>::at(row, col >> 3) + (col & 7);
+            }
+    }
+    __device__ __forceinline__ bf16x8 read(const bf16_t* tile, int t, int dt) const {
+        const bf16_t* p = tile + 16 * t * Tile<DP>::LD;
+        const s16x4 lo = tr(p + off[dt][0]), hi = tr(p + off[dt][1]);
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+    __device__ static __forceinline__ s16x4 tr(const bf16_t* p) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<const s16x4*>(p)));
+    }
+};
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16 splat(float x) {
+    f32x16 v;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = x;
+    return v;
+}
+
+// Results 8 t .. 8 t + 7 of a product, rounded to bf16 (nearest even), as the
+// B operand of step t of the next product.
+__device__ __forceinline__ bf16x8 pack(const f32x16& s, int t) {
+    const u32x4 u = {f32x2_to_bf16x2(s[8 * t], s[8 * t + 1]), f32x2_to_bf16x2(s[8 * t + 2], s[8 * t + 3]),
+                     f32x2_to_bf16x2(s[8 * t + 4], s[8 * t + 5]), f32x2_to_bf16x2(s[8 * t + 6], s[8 * t + 7])};
+    return __builtin_bit_cast(bf16x8, u);
+}
+
+// B operand read straight from memory: row `row` of a row-major matrix (zero
+// where !ok), columns 16 t + 8 half .. + 7.
+template <int DP>
+__device__ __forceinline__ void load_rows(bf16x8 (&f)[DP / 16], const bf16_t* base, int64_t stride, int row, bool ok,
+                                          int d) {
+    const int h = lane_id() >> 5;
+    const bf16_t* p = base + static_cast<int64_t>(row) * stride + 8 * h;
+#pragma unroll
+    for (int t = 0; t < DP / 16; ++t) {
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (ok && 16 * t + 8 * h < d) v = *reinterpret_cast<const u32x4*>(p + 16 * t);
+        f[t] = __builtin_bit_cast(bf16x8, v);
+    }
+}
+
+// Stores a transposed result (column l % 32 = a row of the output, rows = its
+// columns 32 dt ..): the halves swap pieces so that every lane stores 16
+// contiguous bytes.
+template <int DP>
+__device__ __forceinline__ void store_rows(const f32x16 (&o)[DP / 32], float mul, bf16_t* row, bool ok, int d) {
+    const int h = lane_id() >> 5;
+#pragma unroll
+    for (int dt = 0; dt < DP / 32; ++dt)
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int i = 8 * g;
+            // pieces of columns 16 g + 4 half (lo) and 16 g + 8 + 4 half (hi)
+            const u32x2 lo = {f32x2_to_bf16x2(o[dt][i] * mul, o[dt][i + 1] * mul),
+                              f32x2_to_bf16x2(o[dt][i + 2] * mul, o[dt][i + 3] * mul)};
+            const u32x2 hi = {f32x2_to_bf16x2(o[dt][i + 4] * mul, o[dt][i + 5] * mul),
+                              f32x2_to_bf16x2(o[dt][i + 6] * mul, o[dt][i + 7] * mul)};
+            // swap exchanges the first operand's upper half with the second's
+            // lower half: half 0 then holds lo of both halves (columns 16 g ..
+            // 16 g + 7), half 1 hi of both
+            const auto x = __builtin_amdgcn_permlane32_swap(lo.x, hi.x, false, false);
+            const auto y = __builtin_amdgcn_permlane32_swap(lo.y, hi.y, false, false);
+            const u32x4 v = {x[0], y[0], x[1], y[1]};
+            const int col = 32 * dt + 16 * g + 8 * h;
+            if (ok && col < d) *reinterpret_cast<u32x4*>(row + col) = v;
+        }
+}
+
+// What one sequence of the batch sees.
+struct Seq {
+    int n;      // keys (and positions) below this one are real
+    int start;  // position of query 0
+    int pre;    // keys below this one are seen by every query
+    const int32_t* doc;
+};
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+    Seq s;
+    s.n = a.sk;
+    if (a.lengths) {
+        const int len = a.lengths[b];
+        s.n = len < 0 ? 0 : (len < a.sk ? len : a.sk);
+    }
+    int st = a.sk - a.sq;
+    if (a.starts) st = a.starts[b];
+    s.start = st < -kMaxPos ? -kMaxPos : (st > kMaxPos ? kMaxPos : st);
+    s.pre = 0;
+    if (a.prefix) {
+        const int p = a.prefix[b];
+        s.pre = p < 0 ? 0 : (p < s.n ? p : s.n);
+    }
+    s.doc = a.documents ? a.documents + static_cast<int64_t>(b) * a.doc_b : nullptr;
+    return s;
+}
+__device__ __forceinline__ int doc_of(const Seq& s, const AttnArgs& a, int pos) {
+    const int p = pos < 0 ? 0 : (pos < a.sk ? pos : a.sk - 1);
+    return s.doc[p];
+}
+// A query's position is real: with lengths, positions past the length are
+// padding and see nothing.
+__device__ __forceinline__ bool real_row(const Seq& s, const AttnArgs& a, int pos) {
+    return a.lengths == nullptr || pos < s.n;
+}
+
+// Keys one query sees outside the document rule: lo <= j <= hi, or j < pre.
+struct Row {
+    int pos, lo, hi, pre, doc;
+};
+__device__ __forceinline__ Row row_of(const Seq& s, const AttnArgs& a, int pos) {
+    Row r;
+    r.pos = pos;
+    r.lo = 0;
+    r.hi = s.n - 1;
+    r.pre = s.pre;
+    if (a.causal && pos < r.hi) r.hi = pos;
+    if (a.window) {
+        if (pos - a.window + 1 > r.lo) r.lo = pos - a.window + 1;
+        if (pos + a.window - 1 < r.hi) r.hi = pos + a.window - 1;
+    }
+    r.doc = s.doc && a.sk > 0 ? doc_of(s, a, pos) : 0;
+    return r;
+}
+
+// Whether a block of queries at positions [p0, p1] (documents in [d0, d1])
+// sees any key of [j0, j1] (documents in [e0, e1]), and whether every one of
+// those queries sees every one of those keys.  j1 is below n.  `some` may
+// be too generous (elements are then masked one by one), never too strict.
+struct Sight {
+    bool some, all;
+};
+__device__ __forceinline__ Sight sight(const Seq& s, const AttnArgs& a, int p0, int p1, int d0, int d1, int j0, int j1,
+                                       int e0, int e1) {
+    const bool span_some = (!a.causal || j0 <= p1) && (!a.window || (j1 > p0 - a.window && j0 < p1 + a.window));
+    const bool span_all = (!a.causal || j1 <= p0) && (!a.window || (p1 - j0 < a.window && j1 - p0 < a.window));
+    Sight r;
+    r.some = j0 <= j1 && (span_some || j0 < s.pre);
+    r.all = span_all || j1 < s.pre;
+    if (s.doc) {
+        r.some = r.some && e0 <= d1 && d0 <= e1;
+        r.all = r.all && e0 == e1 && d0 == d1 && e0 == d0;
+    }
+    return r;
+}
+
+// Lowest and highest document of the positions [p0, p1] of a sequence, over
+// the wave.
+__device__ __forceinline__ void doc_range(const Seq& s, const AttnArgs& a, int p0, int p1, int& lo, int& hi) {
+    lo = 0x7fffffff;
+    hi = static_cast<int>(0x80000000u);
+    if (!s.doc) return;
+    for (int p = p0 + lane_id(); p <= p1; p += 64) {
+        const int e = doc_of(s, a, p);
+        lo = e < lo ? e : lo;
+        hi = e > hi ? e : hi;
+    }
+#pragma unroll
+    for (int m = 32; m; m >>= 1) {
+        const int x = __shfl_xor(lo, m), y = __shfl_xor(hi, m);
+        lo = x < lo ? x : lo;
+        hi = y > hi ? y : hi;
+    }
+    lo = __builtin_amdgcn_readfirstlane(lo);
+    hi = __builtin_amdgcn_readfirstlane(hi);
+}
+
+// A run of query positions with its documents.
+struct Span {
+    int p0, p1, d0, d1;
+};
+__device__ __forceinline__ Span query_span(const Seq& s, const AttnArgs& a, int i0, int i1) {
+    Span r;
+    r.p0 = s.start + i0;
+    r.p1 = s.start + i1 - 1;
+    if (a.lengths && r.p1 >= s.n) r.p1 = s.n - 1;
+    doc_range(s, a, r.p0, r.p1, r.d0, r.d1);
+    return r;
+}
+
+// The key tiles a workgroup's queries see, in order.  64 tiles are tested at
+// a time, one per lane; the answers stay in scalar registers.
+struct KeyTiles {
+    uint64_t wg, some, all;
+    int base, end;
+    __device__ __forceinline__ void fill(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
+                                         const int2* docs) {
+        const int t = base + lane_id(), j0 = t * kTile;
+        int j1 = j0 + kTile - 1;
+        if (j1 >= s.n) j1 = s.n - 1;
+        int2 e = {0, 0};
+        if (s.doc && t < a.n_tiles) e = docs[t];
+        const bool in = t < end;
+        const Sight x = sight(s, a, g.p0, g.p1, g.d0, g.d1, j0, j1, e.x, e.y);
+        const Sight y = sight(s, a, w.p0, w.p1, w.d0, w.d1, j0, j1, e.x, e.y);
+        wg = __ballot(in && x.some);
+        some = __ballot(in && w.p0 <= w.p1 && y.some);
+        all = __ballot(in && y.all && j0 + kTile <= s.n);
+    }
+    __device__ __forceinline__ void init(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
+                                         const int2* docs) {
+        int lo = 0, hi = s.n - 1;
+        if (a.causal && g.p1 < hi) hi = g.p1;
+        if (a.window) {
+            if (g.p0 - a.window + 1 > lo) lo = g.p0 - a.window + 1;
+            if (g.p1 + a.window - 1 < hi) hi = g.p1 + a.window - 1;
+        }
+        if (s.pre > 0) {
+            lo = 0;
+            if (s.pre - 1 > hi) hi = s.pre - 1;
+        }
+        if (g.p0 > g.p1) hi = -1;
+        base = lo / kTile;
+        end = hi < 0 ? 0 : hi / kTile + 1;
+        wg = some = all = 0;
+        if (base < end) fill(s, a, g, w, docs);
+    }
+    // Next tile, or -1.  mode: 0 this wave sees nothing of it, 1 some, 2 all.
+    __device__ __forceinline__ int next(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
+                                        const int2* docs, int& mode) {
+        while (wg == 0) {
+            base += 64;
+            if (base >= end) return -1;
+            fill(s, a, g, w, docs);
+        }
+        const int i = __builtin_ctzll(wg);
+        wg &= wg - 1;
+        mode = !((some >> i) & 1) ? 0 : (((all >> i) & 1) ? 2 : 1);
+        return base + i;
+    }
+};
+
+// Queries that see one key: those at positions lo .. hi of its document.
+__device__ __forceinline__ Row col_of(const Seq& s, const AttnArgs& a, int j) {
+    Row r;
+    r.pos = j;
+    r.pre = 0;
+    r.lo = s.start;
+    r.hi = s.start + a.sq - 1;
+    if (a.lengths && r.hi >= s.n) r.hi = s.n - 1;
+    if (j >= s.pre) {
+        if (a.causal && j > r.lo) r.lo = j;
+        if (a.window) {
+            if (j - a.window + 1 > r.lo) r.lo = j - a.window + 1;
+            if (j + a.window - 1 < r.hi) r.hi = j + a.window - 1;
+        }
+    }
+    if (j >= s.n) r.hi = r.lo - 1;
+    r.doc = s.doc && a.sk > 0 ? doc_of(s, a, j) : 0;
+    return r;
+}
+
+// The tiles of kTile queries that see a workgroup's keys, as KeyTiles.
+struct QueryTiles {
+    uint64_t wg, some, all;
+    int base, end, rows;
+    __device__ __forceinline__ void fill(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
+                                         const int2* docs) {
+        const int i0 = (base + lane_id()) * kTile;
+        const int i1 = i0 + kTile < rows ? i0 + kTile : rows;
+        const int p0 = s.start + i0, p1 = s.start + i1 - 1;
+        int2 e = {0, 0};
+        if (s.doc && i0 < rows) {
+            const int x = p0 < 0 ? 0 : (p0 < a.sk ? p0 : a.sk - 1), y = p1 < 0 ? 0 : (p1 < a.sk ? p1 : a.sk - 1);
+            const int2 ex = docs[x / kTile], ey = docs[y / kTile];
+            e = {ex.x < ey.x ? ex.x : ey.x, ex.y > ey.y ? ex.y : ey.y};
+        }
+        const bool in = i0 < rows;
+        const Sight x = sight(s, a, p0, p1, e.x, e.y, g.p0, g.p1, g.d0, g.d1);
+        const Sight y = sight(s, a, p0, p1, e.x, e.y, w.p0, w.p1, w.d0, w.d1);
+        wg = __ballot(in && x.some);
+        some = __ballot(in && y.some);
+        all = __ballot(in && y.all && i0 + kTile <= rows);
+    }
+    // rows: queries that are real
+    __device__ __forceinline__ void init(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
+                                         const int2* docs) {
+        rows = a.sq;
+        if (a.lengths && s.n - s.start < rows) rows = s.n - s.start;
+        int lo = 0, hi = rows - 1;
+        if (g.p0 >= s.pre) {
+            if (a.causal && g.p0 - s.start > lo) lo = g.p0 - s.start;
+            if (a.window) {
+                if (g.p0 - a.window + 1 - s.start > lo) lo = g.p0 - a.window + 1 - s.start;
+                if (g.p1 + a.window - 1 - s.start < hi) hi = g.p1 + a.window - 1 - s.start;
+            }
+        }
+        if (g.p0 > g.p1) hi = -1;
+        base = lo / kTile;
+        end = hi < 0 ? 0 : hi / kTile + 1;
+        wg = some = all = 0;
+        if (base < end) fill(s, a, g, w, docs);
+    }
+    __device__ __forceinline__ int next(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
+                                        const int2* docs, int& mode) {
+        while (wg == 0) {
+            base += 64;
+            if (base >= end) return -1;
+            fill(s, a, g, w, docs);
+        }
+        const int i = __builtin_ctzll(wg);
+        wg &= wg - 1;
+        mode = !((some >> i) & 1) ? 0 : (((all >> i) & 1) ? 2 : 1);
+        return base + i;
+    }
+};
+
+// Scores in units of log 2 from the product x = q . k, as p = exp2(z - lse2).
+// cap: z = cap log2e tanh(scale x / cap), with tanh(y) = 1 - 2 / (exp(2 y) +
+// 1), exact to float32 rounding at both ends; r = 1 / (exp(2 y) + 1) gives the
+// derivative 1 - tanh^2 = 4 (r - r^2).
+struct Score {
+    float c;      // scale * log2e (no cap) or 2 scale log2e / cap
+    float a;      // cap * log2e
+    float slope;  // slope * log2e
+};
+template <int MOD>
+__device__ __forceinline__ Score score_of(const AttnArgs& a, int head) {
+    Score s;
+    s.a = a.softcap * kLog2e;
+    s.c = (MOD & kCap) ? 2.0f * a.scale * kLog2e / a.softcap : a.scale * kLog2e;
+    s.slope = (MOD & kBias) ? a.slopes[head] * kLog2e : 0.0f;
+    return s;
+}
+// dist: |query position - key|.  r receives 1 / (exp(2 y) + 1).
+template <int MOD>
+__device__ __forceinline__ float score(const Score& s, float x, float dist, float& r) {
+    float z;
+    if constexpr (MOD & kCap) {
+        r = __builtin_amdgcn_rcpf(exp2_fast(x * s.c) + 1.0f);
+        z = fmaf(-2.0f * s.a, r, s.a);
+    } else {
+        z = x * s.c;
+    }
+    if constexpr (MOD & kBias) z = fmaf(-s.slope, dist, z);
+    return z;
+}
+
+}  // namespace attn
+}  // namespace muon
+
+// fn<DP, MOD>(a, stream) for the head size and the extras of the scores
+#define MUON_ATTN_DISPATCH(fn, a, stream)                                                     \
+    do {                                                                                      \
+        const int mod = ((a).softcap > 0.0f ? kCap : 0) | ((a).slopes ? kBias : 0);           \
+        const int size = (a).d <= 64 ? 64 : ((a).d <= 96 ? 96 : 128);                         \
+        switch (size + mod) {                                                                 \
+            case 64: fn<64, 0>(a, stream); break;                                             \
+            case 65: fn<64, 1>(a, stream); break;                                             \
+            case 66: fn<64, 2>(a, stream); break;                                             \
+            case 67: fn<64, 3>(a, stream); break;                                             \
+            case 96: fn<96, 0>(a, stream); break;                                             \
+            case 97: fn<96, 1>(a, stream); break;                                             \
+            case 98: fn<96, 2>(a, stream); break;                                             \
+            case 99: fn<96, 3>(a, stream); break;                                             \
+            case 128: fn<128, 0>(a, stream); break;                                           \
+            case 129: fn<128, 1>(a, stream); break;                                           \
+            case 130: fn<128, 2>(a, stream); break;                                           \
+            case 131: fn<128, 3>(a, stream); break;                                           \
+        }                                                                                     \
+    } while (0)

@@ -1,0 +1,232 @@
+"""Attention and its gradients on the GPU against the float64 definition, at
+the sizes, layouts and masks where tiles end early or rows see nothing.
+Bounds per element as tests/lm_reference.py derives them."""
+
+import math
+
+import pytest
+import torch
+
+from . import lm_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lm():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from newton_schulz_09_amd import lm as m
+    return m
+
+
+def make(b, sq, sk, hq, hkv, d, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    t = lambda *s, std=1.0: (torch.randn(*s, generator=g) * std).bfloat16().cuda()  # noqa: E731
+    return t(b, sq, hq, d, std=1.5), t(b, sk, hkv, d), t(b, sk, hkv, d), t(b, sq, hq, d)
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32).cuda()
+
+
+def docs(b, sk, mean, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return torch.cumsum((torch.rand(b, sk, generator=g) < 1.0 / mean).int(), 1).int().cuda()
+
+
+def check(lm, q, k, v, dout, backward=True, **kw):
+    print(f"attention q {tuple(q.shape)} k {tuple(k.shape)} {sorted(kw)}", flush=True)
+    want, tol = ref.attention(q, k, v, dout if backward else None, **kw)
+    out, lse = lm.attention(q, k, v, **kw)
+    torch.cuda.synchronize()
+    ref.close(out, want["out"], tol["out"], "out")
+    ref.close(lse, want["lse"], tol["lse"], "lse")
+    if backward:
+        got = lm.attention_backward(dout, q, k, v, out, lse, **kw)
+        torch.cuda.synchronize()
+        for t, name in zip(got, ("dq", "dk", "dv")):
+            ref.close(t, want[name], tol[name], name)
+    return out, lse
+
+
+SHAPES = [
+    (1, 1, 1, 1, 1, 64), (1, 1, 1, 2, 1, 8), (2, 3, 3, 2, 2, 64), (1, 17, 17, 3, 1, 80), (1, 31, 33, 2, 2, 40),
+    (1, 64, 64, 2, 1, 128), (2, 65, 65, 4, 2, 96), (1, 127, 129, 2, 2, 72), (1, 130, 130, 2, 1, 104),
+    (1, 200, 333, 4, 1, 64), (1, 257, 257, 2, 2, 128), (2, 300, 300, 3, 3, 120), (1, 70, 20, 2, 2, 64),
+    (1, 513, 513, 1, 1, 64),
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_shapes(lm, shape, causal):
+    check(lm, *make(*shape), causal=causal)
+
+
+MASKS = {
+    "window 1": dict(window=1), "window 70": dict(window=70), "window both ways": dict(window=33, causal=False),
+    "cap": dict(softcap=5.0), "cap not causal": dict(softcap=30.0, causal=False), "prefix": dict(prefix=(70, 0)),
+    "prefix and window": dict(prefix=(100, 3), window=20), "prefix past the end": dict(prefix=(9999, -5)),
+    "documents": dict(documents=20), "documents not causal": dict(documents=50, causal=False),
+    "documents and prefix": dict(documents=40, prefix=(64, 130)), "slopes": dict(slopes=True),
+    "slopes and cap": dict(slopes=True, softcap=15.0), "lengths": dict(lengths=(150, 64)),
+    "length 0 and 1": dict(lengths=(0, 1)), "length not causal": dict(lengths=(131, 5), causal=False),
+    "length past the end": dict(lengths=(9999, -3)), "starts": dict(starts=(5, 100)),
+    "starts outside": dict(starts=(-50, 190)), "starts far": dict(starts=(2 ** 31 - 1, -2 ** 31)),
+    "scale": dict(scale=0.01),
+    "all": dict(window=90, softcap=20.0, slopes=True, documents=70, lengths=(160, 190), starts=(0, 7)),
+    "all not causal": dict(window=60, softcap=20.0, slopes=True, documents=70, lengths=(160, 190), causal=False),
+}
+
+
+def masks(kw, b, sq, sk, hq):
+    kw = dict(kw)
+    for n in ("prefix", "lengths", "starts"):
+        if n in kw:
+            kw[n] = ints(*kw[n])
+    if "documents" in kw:
+        kw["documents"] = docs(b, sk, kw["documents"])
+    if "slopes" in kw:
+        kw["slopes"] = torch.tensor([2.0 ** -(h + 1) for h in range(hq)]).cuda()
+    return kw
+
+
+@pytest.mark.parametrize("name", MASKS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_masks(lm, name, d):
+    b, s, hq, hkv = 2, 200, 4, 2
+    check(lm, *make(b, s, s, hq, hkv, d), **masks(MASKS[name], b, s, s, hq))
+
+
+@pytest.mark.parametrize("name", MASKS)
+@pytest.mark.parametrize("sq", [1, 5])
+def test_generation_masks(lm, name, sq):
+    b, sk, hq, hkv, d = 2, 200, 4, 2, 64
+    check(lm, *make(b, sq, sk, hq, hkv, d), **masks(MASKS[name], b, sq, sk, hq))
+
+
+@pytest.mark.parametrize("sq,sk,hq,hkv,d", [(1, 5000, 2, 2, 64), (1, 4097, 8, 2, 128), (5, 4500, 12, 3, 80),
+                                            (3, 9000, 32, 1, 64), (33, 5000, 1, 1, 128), (2, 20000, 4, 4, 96)])
+def test_long_caches(lm, sq, sk, hq, hkv, d):
+    q, k, v, dout = make(3, sq, sk, hq, hkv, d)
+    lengths = ints(sk, sk // 2 + 1, 65)
+    starts = (lengths - sq).int()
+    check(lm, q, k, v, dout, backward=sq == 33, lengths=lengths, starts=starts)
+    check(lm, q, k, v, dout, backward=False, window=700, softcap=30.0)
+
+
+def test_unsorted_documents(lm):
+    q, k, v, dout = make(2, 300, 300, 2, 1, 64)
+    g = torch.Generator().manual_seed(3)
+    d = torch.randint(-3, 3, (2, 300), generator=g).int().cuda()
+    d[0, :5] = 2 ** 31 - 1
+    check(lm, q, k, v, dout, documents=d)
+    wide = torch.zeros(2, 700, dtype=torch.int32, device="cuda")
+    wide[:, :300] = d
+    check(lm, q, k, v, dout, documents=wide[:, :300], causal=False)
+
+
+def test_padding_may_hold_anything(lm):
+    q, k, v, dout = make(3, 200, 200, 2, 1, 64)
+    n = (130, 64, 0)
+    for i, x in enumerate(n):
+        for t in (q, k, v, dout):
+            t[i, x:] = float("nan")
+    check(lm, q, k, v, dout, lengths=ints(*n), starts=ints(0, 0, 0))
+    check(lm, q, k, v, dout, lengths=ints(*n), starts=ints(0, 0, 0), causal=False)
+    check(lm, q[:, :1].nan_to_num(), k, v, dout, backward=False, lengths=ints(*n), starts=ints(129, 63, 0))
+
+
+def test_one_projection_and_other_layouts(lm):
+    qkv = make(2, 150, 150, 8, 1, 64)[0]
+    dout = make(2, 150, 150, 4, 1, 64)[3]
+    check(lm, qkv[:, :, :4], qkv[:, :, 4:6], qkv[:, :, 6:], dout)
+    q, k, v, dout = (t.transpose(1, 2) for t in make(2, 4, 4, 150, 150, 64))  # (batch, heads, positions, d) in memory
+    check(lm, q, k, v, dout)
+    one = make(1, 150, 150, 1, 1, 64)[0].expand(2, 150, 4, 64)  # strides of zero
+    check(lm, one, one, one, dout)
+    out = torch.zeros(2, 150, 8, 64, dtype=torch.bfloat16, device="cuda")
+    got, _ = lm.attention(q, k, v, out=out[:, :, 4:])
+    assert got.data_ptr() == out[:, :, 4:].data_ptr() and not out[:, :, :4].any()
+    assert torch.equal(got, lm.attention(q, k, v)[0])
+
+
+def test_large_scores(lm):
+    q, k, v, dout = make(1, 100, 100, 2, 2, 64)
+    check(lm, q * 8, k * 8, v, dout)
+    check(lm, q * 8, k * 8, v, dout, softcap=50.0)
+    q[:, :, :, :] = 0
+    out, lse = lm.attention(q, k, v)
+    assert torch.allclose(lse[0, 0].cpu(), torch.log(torch.arange(1.0, 101.0)), atol=1e-5)
+
+
+def test_empty(lm):
+    q, k, v, dout = make(2, 5, 0, 2, 1, 64)
+    out, lse = lm.attention(q, k, v)
+    assert not out.any() and torch.isneginf(lse).all()
+    dq, dk, dv = lm.attention_backward(dout, q, k, v, out, lse)
+    assert not dq.any() and dk.numel() == 0
+    q, k, v, dout = make(2, 0, 5, 2, 1, 64)
+    out, lse = lm.attention(q, k, v)
+    dq, dk, dv = lm.attention_backward(dout, q, k, v, out, lse)
+    assert out.numel() == 0 and not dk.any() and not dv.any()
+    assert lm.attention(*make(0, 5, 5, 2, 1, 64)[:3])[0].shape == (0, 5, 2, 64)
+
+
+def test_same_bits_and_other_streams(lm):
+    q, k, v, dout = make(2, 300, 300, 4, 2, 128)
+    run = lambda: lm.attention(q, k, v) + lm.attention_backward(dout, q, k, v, *lm.attention(q, k, v))  # noqa: E731
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run()
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("sq", [1, 260])
+def test_graph(lm, sq):
+    q, k, v, dout = make(2, sq, 2100, 4, 2, 64)
+    d = docs(2, 2100, 900)
+
+    def run():
+        out, lse = lm.attention(q, k, v, documents=d, softcap=20.0)
+        return (out, lse, *lm.attention_backward(dout, q, k, v, out, lse, documents=d, softcap=20.0))
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for seed in range(3):
+        for t, new in zip((q, k, v, dout), make(2, sq, 2100, 4, 2, 64, seed=seed)):
+            t.copy_(new)
+        want = run()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), seed
+
+
+def test_gradient_against_differences(lm):
+    """d(loss)/d(step) of a step along random directions, loss = sum out * dout
+    in float64 at the float64 definition: the kernels' gradients predict it."""
+    q, k, v, dout = make(1, 90, 90, 4, 2, 64)
+    kw = dict(softcap=10.0, slopes=torch.tensor([0.5, 0.25, 0.1, 0.0]).cuda(), window=40)
+    out, lse = lm.attention(q, k, v, **kw)
+    grads = lm.attention_backward(dout, q, k, v, out, lse, **kw)
+    g = torch.Generator().manual_seed(9)
+    dirs = [torch.randn(t.shape, generator=g, dtype=torch.float64) for t in (q, k, v)]
+    eps = 1e-4
+
+    def loss(s):
+        r, _ = ref.attention(*[t.cpu().double() + s * x for t, x in zip((q, k, v), dirs)], **kw)
+        return (r["out"] * dout.cpu().double()).sum().item()
+
+    slope = (loss(eps) - loss(-eps)) / (2 * eps)
+    want, tol = ref.attention(q, k, v, dout, **kw)
+    pred = sum((t.cpu().double() * x).sum().item() for t, x in zip(grads, dirs))
+    room = sum((tol[n] * x.abs()).sum().item() for n, x in zip(("dq", "dk", "dv"), dirs))
+    assert math.isfinite(pred) and abs(pred - slope) <= room + 1e-4 * abs(slope)
