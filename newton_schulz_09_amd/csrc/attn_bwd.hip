@@ -3,8 +3,6 @@
 // walked per block of queries, then dK and dV with the queries walked per
 // block of keys.  P is made again from the scores and lse; recomputing the
 // two products S and dO V^T costs 7 products instead of 5.
-#include <type_traits>
-
 #include "attn_common.hpp"
 
 namespace muon {
@@ -13,175 +11,188 @@ namespace {
 
 using namespace attn;
 
-// p and dS of 16 results: s holds q . k, dp holds dO . v - delta.  lse2 in
-// units of log 2.
+// Result i of a block: s holds q . k (minus lse in the product's units where
+// there are no extras), dp holds dO . v - delta; they become P and dS.
 template <int MOD>
 __device__ __forceinline__ void grad1(const Score& sc, f32x16& s, f32x16& dp, int i, float lse2, float dist) {
     float r = 0.0f;
-    const float p = exp2_fast(MOD ? score<MOD>(sc, s[i], dist, r) - lse2 : fmaf(s[i], sc.c, -lse2));
+    const float p = exp2_fast(MOD ? score<MOD>(sc, s[i], dist, r) - lse2 : s[i] * sc.c);
     float ds = p * dp[i];
     if constexpr (MOD & kCap) ds *= 4.0f * fmaf(-r, r, r);
     s[i] = p;
     dp[i] = ds;
 }
 
-// The row statistic the kernels subtract: a row that saw nothing has lse
-// -inf, and +inf makes its P zero.
-__device__ __forceinline__ float lse2_of(float lse) { return lse == neg_inf() ? __builtin_inff() : lse * kLog2e; }
+// What the kernels subtract from a row's scores: with extras lse in units of
+// log 2, +inf for a row that saw nothing (its P is then zero); without, -lse
+// in units of the product q . k, where the sums of the products start.
+template <int MOD>
+__device__ __forceinline__ float lse_term(float lse, float scale) {
+    if constexpr (MOD != 0) return lse == neg_inf() ? __builtin_inff() : lse * kLog2e;
+    else return lse == neg_inf() ? neg_inf() : -lse / scale;
+}
 
-template <int DP, int QB, int NW, int MOD>
-__global__ __launch_bounds__(64 * NW, QB == 1 ? 2 : 1) void k_attn_dq(const AttnArgs a) {
-    constexpr int BM = 32 * QB * NW, NT = 64 * NW;
-    __shared__ __align__(16) bf16_t lds[2][2][Tile<DP>::ELEMS];
-    __shared__ __align__(16) int sdocs[2][kTile];
-    const int H = a.b * a.hq, U = a.b * a.hkv;
+constexpr int kAhead = 3;
+
+// dQ.  32 keys are one block; the gradients of the scores of a block are made
+// in the shadow of products of the other block of the tile:
+//     products   S, dP (0)   S, dP (1)   dQ (0)    dQ (1)
+//     vector                 block 0     block 1
+template <int DP, int NW, int ST, int MOD>
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
+    constexpr int BM = 32 * NW, NT = 64 * NW, TB = 2 * Tile<DP>::ELEMS;
+    static_assert(ST == 2 || ST == 3, "the waits below count one tile ahead");
+    __shared__ __align__(16) bf16_t lds[ST][2][Tile<DP>::ELEMS];
+    __shared__ __align__(16) int sdocs[ST][kTile];
+    const Args a = arguments();
+    const int H = a->b * a->hq, U = a->b * a->hkv;
     const int blk = blockIdx.x, e = blk % H;
-    const int u = e % U, b = u / a.hkv, kvh = u % a.hkv, h = kvh * a.grp + e / U;
+    const int u = e % U, b = u / a->hkv, kvh = u % a->hkv, h = kvh * a->grp + e / U;
     const int i0 = ((gridDim.x / H) - 1 - blk / H) * BM;
-    const int i1 = i0 + BM < a.sq ? i0 + BM : a.sq;
+    const int i1 = i0 + BM < a->sq ? i0 + BM : a->sq;
     const Seq seq = sequence(a, b);
-    const int w0 = i0 + wave_id() * 32 * QB, w1 = w0 + 32 * QB < a.sq ? w0 + 32 * QB : a.sq;
+    const int w0 = i0 + wave_id() * 32, w1 = w0 + 32 < a->sq ? w0 + 32 : a->sq;
     const Span g = query_span(seq, a, i0, i1), w = query_span(seq, a, w0, w1);
-    const int2* docs = a.doc_tiles + static_cast<int64_t>(b) * a.n_tiles;
 
-    bf16x8 qf[QB][DP / 16], dof[QB][DP / 16];
-    Row row[QB];
-    float lse2[QB], delta[QB];
-    const Score sc = score_of<MOD>(a, h);
+    Direct<DP, NT> lk, lv;
+    lk.init(a->k + b * a->k_b + kvh * a->k_h, a->k_s, seq.n, a->d);
+    lv.init(a->v + b * a->v_b + kvh * a->v_h, a->v_s, seq.n, a->d);
+    const uint32_t at = lds_addr(lds);
+    const int sk = a->sk;
+    KeyTiles it;
+    it.init(seq, a, g, w);
+    int tile[ST], mode[ST];
+    auto fetch = [&](int x) {
+        tile[x] = it.next(seq, a, g, w, mode[x]);
+        if (tile[x] < 0) return;
+        lk.load(tile[x] * kTile, at + 2 * x * TB);
+        lv.load(tile[x] * kTile, at + (2 * x + 1) * TB);
+        if (seq.doc) load_values(seq.doc, tile[x] * kTile, sk, lds_addr(sdocs[x]));
+    };
 #pragma unroll
-    for (int x = 0; x < QB; ++x) {
-        const int i = w0 + 32 * x + (lane_id() & 31);
-        row[x] = row_of(seq, a, seq.start + i);
-        const bool ok = i < a.sq && real_row(seq, a, seq.start + i);
-        load_rows<DP>(qf[x], a.q + b * a.q_b + h * a.q_h, a.q_s, i, ok, a.d);
-        load_rows<DP>(dof[x], a.dout + b * a.do_b + h * a.do_h, a.do_s, i, ok, a.d);
+    for (int x = 0; x < ST - 1; ++x) fetch(x);
+
+    const int i = w0 + (lane_id() & 31);
+    const Row row = row_of(seq, a, seq.start + i);
+    const bool real = i < a->sq && real_row(seq, a, seq.start + i);
+    const Score sc = score_of<MOD>(a, h);
+    bf16x8 qf[DP / 16], dof[DP / 16];
+    load_rows<DP>(qf, a->q + b * a->q_b + h * a->q_h, a->q_s, i, real, a->d);
+    load_rows<DP>(dof, a->dout + b * a->do_b + h * a->do_h, a->do_s, i, real, a->d);
+    float delta = 0.0f;
+    {
         bf16x8 of[DP / 16];
-        load_rows<DP>(of, a.out + b * a.o_b + h * a.o_h, a.o_s, i, ok, a.d);
-        float sum = 0.0f;
+        load_rows<DP>(of, a->out + b * a->o_b + h * a->o_h, a->o_s, i, real, a->d);
 #pragma unroll
         for (int t = 0; t < DP / 16; ++t)
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                sum = fmaf(static_cast<float>(dof[x][t][c]), static_cast<float>(of[t][c]), sum);
-        delta[x] = half_sum(sum);
-        const int64_t at = (static_cast<int64_t>(b) * a.hq + h) * a.sq + i;
-        lse2[x] = ok ? lse2_of(a.lse[at]) : __builtin_inff();
-        if (i < a.sq && lane_id() < 32) a.delta[at] = delta[x];
+            for (int c = 0; c < 8; ++c) delta = fmaf(static_cast<float>(dof[t][c]), static_cast<float>(of[t][c]), delta);
+        delta = half_sum(delta);
     }
-    Loader<DP, NT> lk, lv;
-    lk.init(a.k + b * a.k_b + kvh * a.k_h, a.k_s, seq.n, a.d);
-    lv.init(a.v + b * a.v_b + kvh * a.v_h, a.v_s, seq.n, a.d);
+    const int64_t stat = (static_cast<int64_t>(b) * a->hq + h) * a->sq + i;
+    const float lse = lse_term<MOD>(real ? a->lse[stat] : neg_inf(), a->scale);
+    if (i < a->sq && lane_id() < 32) {
+        // for the second kernel: what it starts its products from
+        a->stats[stat] = lse;
+        a->stats[stat + a->delta_at] = -delta;
+    }
     RowFrag<DP> rf;
     ColFrag<DP> cf;
     rf.init();
     cf.init();
-    f32x16 dq[QB][DP / 32];
+    f32x16 dq[DP / 32];
 #pragma unroll
-    for (int x = 0; x < QB; ++x)
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) dq[x][dt] = splat(0.0f);
+    for (int dt = 0; dt < DP / 32; ++dt) dq[dt] = splat(0.0f);
+    settle(qf);
+    settle(dof);
 
-    auto step = [&](auto masked, const bf16_t* sk, const bf16_t* sv, const int* sdoc, int k0) {
+    constexpr int KT = DP / 16, DT = DP / 32;
+    auto step = [&](uint32_t tk, uint32_t tv, bool masked, const int* sdoc, int k0) {
         const int h4 = 4 * (lane_id() >> 5);
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            f32x16 s[QB], dp[QB];
-#pragma unroll
-            for (int x = 0; x < QB; ++x) {
-                s[x] = splat(0.0f);
-                dp[x] = splat(-delta[x]);
+        f32x16 s[2], dp[2];
+        bf16x8 p[2][2], ring[kAhead];
+        float s0 = MOD ? 0.0f : lse, dp0 = -delta;
+        asm volatile("" : "+v"(s0), "+v"(dp0));  // (their 16 copies are not kept between tiles)
+        auto operand = [&](int y) {  // K and V along the row in turn, both blocks; then K across
+            return y < 4 * KT ? rf.read(y % 2 ? tv : tk, y / (2 * KT), y % (2 * KT) / 2)
+                              : cf.read(tk, (y - 4 * KT) / DT, (y - 4 * KT) % DT);
+        };
+        auto grads = [&](int kb, int i) {
+            grad1<MOD>(sc, s[kb], dp[kb], i, lse,
+                       fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + 8 * (i / 4) + i % 4)));
+        };
+        auto finish = [&](int kb) {
+            if (masked) {
+                const Hide hide = hide_of(row, seq, a, k0, h4);
+                each<0, 16>([&](auto i_) {
+                    constexpr int i = decltype(i_)::value;
+                    if (!seen(hide, 32 * kb + 8 * (i / 4) + i % 4, sdoc ? sdoc + h4 : nullptr)) dp[kb][i] = 0.0f;
+                });
             }
-#pragma unroll
-            for (int t = 0; t < DP / 16; ++t) {
-                const bf16x8 kf = rf.read(sk, kb, t), vf = rf.read(sv, kb, t);
-#pragma unroll
-                for (int x = 0; x < QB; ++x) {
-                    s[x] = mfma(kf, qf[x][t], s[x]);
-                    dp[x] = mfma(vf, dof[x][t], dp[x]);
-                }
+            p[kb][0] = pack(dp[kb], 0);
+            p[kb][1] = pack(dp[kb], 1);
+        };
+        each<0, kAhead>([&](auto y) { ring[y] = operand(y); });
+        in_order();
+        each<0, 6 * KT>([&](auto y_) {
+            constexpr int y = decltype(y_)::value;
+            if constexpr (y < 4 * KT) {
+                constexpr int kb = y / (2 * KT), t = y % (2 * KT) / 2;
+                if constexpr (y % 2 == 0) s[kb] = mfma(ring[y % kAhead], qf[t], t == 0 ? splat(s0) : s[kb]);
+                else dp[kb] = mfma(ring[y % kAhead], dof[t], t == 0 ? splat(dp0) : dp[kb]);
+            } else {
+                constexpr int x = y - 4 * KT, dt = x % DT, kb = x / (2 * DT), t = x / DT % 2;
+                dq[dt] = mfma(ring[y % kAhead], p[kb][t], dq[dt]);
             }
-            bf16x8 p[QB][2];
-#pragma unroll
-            for (int x = 0; x < QB; ++x) {
-                const float base = static_cast<float>(row[x].pos - k0 - h4);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    grad1<MOD>(sc, s[x], dp[x], i, lse2[x],
-                               fabsf(base - static_cast<float>(32 * kb + 8 * (i / 4) + i % 4)));
-                if constexpr (decltype(masked)::value) {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = 32 * kb + 8 * (i / 4) + h4 + i % 4, jj = k0 + j;
-                        bool vis = (jj >= row[x].lo && jj <= row[x].hi) || jj < row[x].pre;
-                        if (sdoc) vis = vis && sdoc[j] == row[x].doc;
-                        if (!vis) dp[x][i] = 0.0f;
-                    }
-                }
-                p[x][0] = pack(dp[x], 0);
-                p[x][1] = pack(dp[x], 1);
+            if constexpr (y + kAhead < 6 * KT) ring[y % kAhead] = operand(y + kAhead);
+            if constexpr (y >= 2 * KT + 2 && y < 4 * KT) {
+                constexpr int x = y - 2 * KT - 2, n = 2 * KT - 2;
+                each<16 * x / n, 16 * (x + 1) / n>([&](auto i) { grads(0, i); });
             }
+            if constexpr (y == 4 * KT - 1) finish(0);
+            if constexpr (y >= 4 * KT && y < 5 * KT) {
+                constexpr int x = y - 4 * KT;
+                each<16 * x / KT, 16 * (x + 1) / KT>([&](auto i) { grads(1, i); });
+            }
+            if constexpr (y == 5 * KT - 1) finish(1);
+            in_order();
+        });
+    };
+    for (;;) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int dt = 0; dt < DP / 32; ++dt) {
-                    const bf16x8 kf = cf.read(sk, 2 * kb + t, dt);
-#pragma unroll
-                    for (int x = 0; x < QB; ++x) dq[x][dt] = mfma(kf, p[x][t], dq[x][dt]);
-                }
+        for (int x = 0; x < ST; ++x) {
+            constexpr int NL = 2 * Direct<DP, NT>::N;
+            if (tile[x] < 0) goto done;
+            if (ST == 2 || tile[(x + 1) % ST] < 0) landed<0>();
+            else if (seq.doc) landed<(ST - 2) * (NL + 1)>();
+            else landed<(ST - 2) * NL>();
+            fetch((x + ST - 1) % ST);
+            if (mode[x] != 0)
+                step(at + 2 * x * TB, at + (2 * x + 1) * TB, mode[x] == 1, seq.doc ? sdocs[x] : nullptr, tile[x] * kTile);
         }
-    };
-
-    KeyTiles it;
-    it.init(seq, a, g, w, docs);
-    int mode = 0, dcur = 0;
-    int t = it.next(seq, a, g, w, docs, mode);
-    auto load = [&](int tile) {
-        lk.load(tile * kTile);
-        lv.load(tile * kTile);
-        if (seq.doc && threadIdx.x < kTile) dcur = doc_of(seq, a, tile * kTile + threadIdx.x);
-    };
-    auto store = [&](int buf) {
-        lk.store(lds[buf][0]);
-        lv.store(lds[buf][1]);
-        if (seq.doc && threadIdx.x < kTile) sdocs[buf][threadIdx.x] = dcur;
-    };
-    if (t >= 0) {
-        load(t);
-        store(0);
     }
-    int buf = 0;
-    while (t >= 0) {
-        __syncthreads();
-        int nmode = 0;
-        const int nt = it.next(seq, a, g, w, docs, nmode);
-        if (nt >= 0) load(nt);
-        if (mode == 2) step(std::false_type{}, lds[buf][0], lds[buf][1], nullptr, t * kTile);
-        else if (mode == 1) step(std::true_type{}, lds[buf][0], lds[buf][1], seq.doc ? sdocs[buf] : nullptr, t * kTile);
-        if (nt >= 0) store(buf ^ 1);
-        buf ^= 1;
-        t = nt;
-        mode = nmode;
-    }
-#pragma unroll
-    for (int x = 0; x < QB; ++x) {
-        const int i = w0 + 32 * x + (lane_id() & 31);
-        // dq is contiguous (b, sq, hq, d)
-        bf16_t* o = a.dq + ((static_cast<int64_t>(b) * a.sq + i) * a.hq + h) * a.d;
-        store_rows<DP>(dq[x], a.scale, o, i < a.sq, a.d);
-    }
+done:
+    const Args z = again(a);
+    // dq is contiguous (b, sq, hq, d)
+    store_rows<DP>(dq, z->scale, z->dq + ((static_cast<int64_t>(b) * z->sq + i) * z->hq + h) * z->d, i < z->sq, z->d);
 }
 
-template <int DP, int KB, int NW, int MOD>
-__global__ __launch_bounds__(64 * NW, 1) void k_attn_dkv(const AttnArgs a) {
-    constexpr int BN = 32 * KB * NW, NT = 64 * NW;
-    __shared__ __align__(16) bf16_t lds[2][2][Tile<DP>::ELEMS];
-    __shared__ __align__(16) int sdocs[2][kTile];
-    __shared__ __align__(16) float sstat[2][2][kTile];
-    const int U = a.b * a.hkv;
-    const int blk = blockIdx.x, u = blk % U, b = u / a.hkv, kvh = u % a.hkv;
+// dK and dV of 32 NW keys, walked over the queries of every head that shares
+// them.  32 queries are one block of a tile; as above
+//     products   S, dP (0)   S, dP (1)   dV, dK (0)   dV, dK (1)
+//     vector                 block 0     block 1
+template <int DP, int NW, int ST, int MOD>
+__global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const AttnArgs) {
+    constexpr int BN = 32 * NW, NT = 64 * NW, TB = 2 * Tile<DP>::ELEMS;
+    static_assert(ST == 2 || ST == 3, "the waits below count one tile ahead");
+    __shared__ __align__(16) bf16_t lds[ST][2][Tile<DP>::ELEMS];
+    __shared__ __align__(16) float sstat[ST][2][kTile];
+    const Args a = arguments();
+    const int U = a->b * a->hkv;
+    const int blk = blockIdx.x, u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
     const int j0 = blk / U * BN;
     const Seq seq = sequence(a, b);
-    const int w0 = j0 + wave_id() * 32 * KB;
+    const int w0 = j0 + wave_id() * 32;
     auto key_span = [&](int lo, int hi) {
         Span r;
         r.p0 = lo;
@@ -189,175 +200,157 @@ __global__ __launch_bounds__(64 * NW, 1) void k_attn_dkv(const AttnArgs a) {
         doc_range(seq, a, r.p0, r.p1, r.d0, r.d1);
         return r;
     };
-    const Span g = key_span(j0, j0 + BN), w = key_span(w0, w0 + 32 * KB);
+    const Span g = key_span(j0, j0 + BN), w = key_span(w0, w0 + 32);
     // whole blocks of real keys only: the rest is masked one by one
-    const bool whole = w0 + 32 * KB <= seq.n;
-    const int2* docs = a.doc_tiles + static_cast<int64_t>(b) * a.n_tiles;
+    const bool whole = w0 + 32 <= seq.n;
+    const int j = w0 + (lane_id() & 31);
+    const Col col = col_of(seq, a, j);
+    bf16x8 kf[DP / 16], vf[DP / 16];
+    load_rows<DP>(kf, a->k + b * a->k_b + kvh * a->k_h, a->k_s, j, j < seq.n, a->d);
+    load_rows<DP>(vf, a->v + b * a->v_b + kvh * a->v_h, a->v_s, j, j < seq.n, a->d);
 
-    bf16x8 kf[KB][DP / 16], vf[KB][DP / 16];
-    Row col[KB];
+    // the tiles of all the heads that share the keys, one after the other
+    QueryTiles it;
+    it.init(seq, a, g, w);
+    Direct<DP, NT> lq, ld;
+    lq.init(a->q + b * a->q_b + static_cast<int64_t>(kvh) * a->grp * a->q_h, a->q_s, it.rows, a->d);
+    ld.init(a->dout + b * a->do_b + static_cast<int64_t>(kvh) * a->grp * a->do_h, a->do_s, it.rows, a->d);
+    const float* stat = a->stats + (static_cast<int64_t>(b) * a->hq + kvh * a->grp) * a->sq;
+    const uint32_t at = lds_addr(lds);
+    int tile[ST], mode[ST], left = a->grp - 1;
+    Score sc[ST];
+    Score now = score_of<MOD>(a, kvh * a->grp);
+    auto fetch = [&](int x) {
+        tile[x] = it.next(seq, a, g, w, mode[x]);
+        if (tile[x] < 0 && left > 0) {
+            const Args z = again(a);
+            --left;
+            it.init(seq, z, g, w);
+            lq.base += z->q_h;
+            ld.base += z->do_h;
+            stat += z->sq;
+            now = score_of<MOD>(z, kvh * z->grp + z->grp - 1 - left);
+            tile[x] = it.next(seq, z, g, w, mode[x]);
+        }
+        sc[x] = now;
+        if (tile[x] < 0) return;
+        const int row0 = tile[x] * kTile;
+        lq.load(row0, at + 2 * x * TB);
+        ld.load(row0, at + (2 * x + 1) * TB);
+        load_values(stat, row0, it.rows, lds_addr(sstat[x][0]));
+        load_values(stat + again(a)->delta_at, row0, it.rows, lds_addr(sstat[x][1]));
+    };
 #pragma unroll
-    for (int x = 0; x < KB; ++x) {
-        const int j = w0 + 32 * x + (lane_id() & 31);
-        col[x] = col_of(seq, a, j);
-        load_rows<DP>(kf[x], a.k + b * a.k_b + kvh * a.k_h, a.k_s, j, j < seq.n, a.d);
-        load_rows<DP>(vf[x], a.v + b * a.v_b + kvh * a.v_h, a.v_s, j, j < seq.n, a.d);
-    }
+    for (int x = 0; x < ST - 1; ++x) fetch(x);
     RowFrag<DP> rf;
     ColFrag<DP> cf;
     rf.init();
     cf.init();
-    f32x16 dk[KB][DP / 32], dv[KB][DP / 32];
+    f32x16 dk[DP / 32], dv[DP / 32];
 #pragma unroll
-    for (int x = 0; x < KB; ++x)
-#pragma unroll
-        for (int dt = 0; dt < DP / 32; ++dt) dk[x][dt] = dv[x][dt] = splat(0.0f);
+    for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = dv[dt] = splat(0.0f);
+    settle(kf);
+    settle(vf);
 
-    for (int r = 0; r < a.grp; ++r) {
-        const int h = kvh * a.grp + r;
-        const Score sc = score_of<MOD>(a, h);
-        const float inv_scale = 1.0f / a.scale;
-        QueryTiles it;
-        it.init(seq, a, g, w, docs);
-        Loader<DP, NT> lq, ld;
-        lq.init(a.q + b * a.q_b + h * a.q_h, a.q_s, it.rows, a.d);
-        ld.init(a.dout + b * a.do_b + h * a.do_h, a.do_s, it.rows, a.d);
-        const int64_t stat = (static_cast<int64_t>(b) * a.hq + h) * a.sq;
-        float st0 = 0.0f, st1 = 0.0f;
-        int dcur = 0;
-
-        // s starts at -lse in units of the product (no extras), dp at -delta
-        auto step = [&](auto masked, const bf16_t* sq, const bf16_t* sd, const float* sl, const float* sdel,
-                        const int* sdoc, int q0) {
-            const int h4 = 4 * (lane_id() >> 5);
-#pragma unroll
-            for (int qb = 0; qb < 2; ++qb) {
-                f32x16 s[KB], dp[KB], lse;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int at = 32 * qb + 8 * (i / 4) + h4 + i % 4;
-                    lse[i] = sl[at];
-                    dp[0][i] = sdel[at];
-                }
-#pragma unroll
-                for (int x = KB - 1; x >= 0; --x) {
-                    dp[x] = dp[0];
-                    s[x] = MOD ? splat(0.0f) : lse;
-                }
-#pragma unroll
-                for (int t = 0; t < DP / 16; ++t) {
-                    const bf16x8 qa = rf.read(sq, qb, t), da = rf.read(sd, qb, t);
-#pragma unroll
-                    for (int x = 0; x < KB; ++x) {
-                        s[x] = mfma(qa, kf[x][t], s[x]);
-                        dp[x] = mfma(da, vf[x][t], dp[x]);
-                    }
-                }
-                bf16x8 pp[KB][2], pd[KB][2];
-#pragma unroll
-                for (int x = 0; x < KB; ++x) {
-                    const float base = static_cast<float>(seq.start + q0 + h4 - col[x].pos);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        grad1<MOD>(sc, s[x], dp[x], i, MOD ? lse[i] : 0.0f,
-                                   fabsf(base + static_cast<float>(32 * qb + 8 * (i / 4) + i % 4)));
-                    if constexpr (decltype(masked)::value) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int at = 32 * qb + 8 * (i / 4) + h4 + i % 4, p = seq.start + q0 + at;
-                            bool vis = p >= col[x].lo && p <= col[x].hi;
-                            if (sdoc) vis = vis && sdoc[at] == col[x].doc;
-                            if (!vis) s[x][i] = dp[x][i] = 0.0f;
-                        }
-                    }
-                    pp[x][0] = pack(s[x], 0);
-                    pp[x][1] = pack(s[x], 1);
-                    pd[x][0] = pack(dp[x], 0);
-                    pd[x][1] = pack(dp[x], 1);
-                }
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-#pragma unroll
-                    for (int dt = 0; dt < DP / 32; ++dt) {
-                        const bf16x8 da = cf.read(sd, 2 * qb + t, dt), qa = cf.read(sq, 2 * qb + t, dt);
-#pragma unroll
-                        for (int x = 0; x < KB; ++x) {
-                            dv[x][dt] = mfma(da, pp[x][t], dv[x][dt]);
-                            dk[x][dt] = mfma(qa, pd[x][t], dk[x][dt]);
-                        }
-                    }
-            }
+    constexpr int KT = DP / 16, DT = DP / 32;
+    auto step = [&](uint32_t tq, uint32_t td, const float* sl, const float* sdel, bool masked, const Score& score, int q0) {
+        const int h4 = 4 * (lane_id() >> 5);
+        f32x16 s[2], dp[2];
+        bf16x8 pp[2][2], pd[2][2], ring[kAhead];
+        auto operand = [&](int y) {  // Q and dO along the row in turn, both blocks; then dO and Q across
+            return y < 4 * KT ? rf.read(y % 2 ? td : tq, y / (2 * KT), y % (2 * KT) / 2)
+                              : cf.read(y % 2 ? tq : td, (y - 4 * KT) / 2 / DT, (y - 4 * KT) / 2 % DT);
         };
-
-        auto load = [&](int tile) {
-            lq.load(tile * kTile);
-            ld.load(tile * kTile);
-            if (threadIdx.x < kTile) {
-                const int i = tile * kTile + threadIdx.x;
-                float l = __builtin_inff(), d = 0.0f;
-                if (i < it.rows) {
-                    l = lse2_of(a.lse[stat + i]);
-                    d = a.delta[stat + i];
-                }
-                st0 = MOD ? l : -l * kLn2 * inv_scale;
-                st1 = -d;
-                if (seq.doc) dcur = doc_of(seq, a, seq.start + i);
-            }
+        auto starts = [&](int qb) {
+            each<0, 16>([&](auto i_) {
+                constexpr int i = decltype(i_)::value;
+                const int r = 32 * qb + 8 * (i / 4) + h4 + i % 4;
+                s[qb][i] = MOD ? 0.0f : sl[r];
+                dp[qb][i] = sdel[r];
+            });
         };
-        auto store = [&](int buf) {
-            lq.store(lds[buf][0]);
-            ld.store(lds[buf][1]);
-            if (threadIdx.x < kTile) {
-                sstat[buf][0][threadIdx.x] = st0;
-                sstat[buf][1][threadIdx.x] = st1;
-                if (seq.doc) sdocs[buf][threadIdx.x] = dcur;
-            }
+        auto grads = [&](int qb, int i) {
+            const int r = 32 * qb + 8 * (i / 4) + i % 4;
+            grad1<MOD>(score, s[qb], dp[qb], i, MOD ? sl[r + h4] : 0.0f,
+                       fabsf(static_cast<float>(seq.start + q0 + h4 - col.pos) + static_cast<float>(r)));
         };
-        int mode = 0;
-        int t = it.next(seq, a, g, w, docs, mode);
-        if (r > 0) __syncthreads();  // the last head's tiles are read
-        if (t >= 0) {
-            load(t);
-            store(0);
-        }
-        int buf = 0;
-        while (t >= 0) {
-            __syncthreads();
-            int nmode = 0;
-            const int nt = it.next(seq, a, g, w, docs, nmode);
-            if (nt >= 0) load(nt);
-            const int* sdoc = seq.doc ? sdocs[buf] : nullptr;
-            if (mode == 2 && whole)
-                step(std::false_type{}, lds[buf][0], lds[buf][1], sstat[buf][0], sstat[buf][1], nullptr, t * kTile);
-            else if (mode != 0)
-                step(std::true_type{}, lds[buf][0], lds[buf][1], sstat[buf][0], sstat[buf][1], sdoc, t * kTile);
-            if (nt >= 0) store(buf ^ 1);
-            buf ^= 1;
-            t = nt;
-            mode = nmode;
+        auto finish = [&](int qb) {
+            if (masked) {
+                const Args z = again(a);
+                each<0, 16>([&](auto i_) {
+                    constexpr int i = decltype(i_)::value;
+                    const int p = seq.start + q0 + 32 * qb + 8 * (i / 4) + h4 + i % 4;
+                    bool vis = p >= col.lo && p <= col.hi;
+                    if (seq.doc) vis = vis && doc_of(seq, z, p) == col.doc;
+                    if (!vis) s[qb][i] = dp[qb][i] = 0.0f;
+                });
+            }
+            pp[qb][0] = pack(s[qb], 0);
+            pp[qb][1] = pack(s[qb], 1);
+            pd[qb][0] = pack(dp[qb], 0);
+            pd[qb][1] = pack(dp[qb], 1);
+        };
+        starts(0);
+        each<0, kAhead>([&](auto y) { ring[y] = operand(y); });
+        in_order();
+        each<0, 8 * KT>([&](auto y_) {
+            constexpr int y = decltype(y_)::value;
+            if constexpr (y < 4 * KT) {
+                constexpr int qb = y / (2 * KT), t = y % (2 * KT) / 2;
+                if constexpr (y % 2 == 0) s[qb] = mfma(ring[y % kAhead], kf[t], s[qb]);
+                else dp[qb] = mfma(ring[y % kAhead], vf[t], dp[qb]);
+            } else {
+                constexpr int x = (y - 4 * KT) / 2, dt = x % DT, qb = x / (2 * DT), t = x / DT % 2;
+                if constexpr (y % 2 == 0) dv[dt] = mfma(ring[y % kAhead], pp[qb][t], dv[dt]);
+                else dk[dt] = mfma(ring[y % kAhead], pd[qb][t], dk[dt]);
+            }
+            if constexpr (y + kAhead < 8 * KT) ring[y % kAhead] = operand(y + kAhead);
+            if constexpr (y == KT) starts(1);
+            if constexpr (y >= 2 * KT + 2 && y < 4 * KT) {
+                constexpr int x = y - 2 * KT - 2, n = 2 * KT - 2;
+                each<16 * x / n, 16 * (x + 1) / n>([&](auto i) { grads(0, i); });
+            }
+            if constexpr (y == 4 * KT - 1) finish(0);
+            if constexpr (y >= 4 * KT + 1 && y < 6 * KT) {
+                constexpr int x = y - 4 * KT - 1, n = 2 * KT - 1;
+                each<16 * x / n, 16 * (x + 1) / n>([&](auto i) { grads(1, i); });
+            }
+            if constexpr (y == 6 * KT - 1) finish(1);
+            in_order();
+        });
+    };
+    for (;;) {
+#pragma unroll
+        for (int x = 0; x < ST; ++x) {
+            constexpr int NL = 2 * Direct<DP, NT>::N + 2;
+            if (tile[x] < 0) goto done;
+            if (ST == 2 || tile[(x + 1) % ST] < 0) landed<0>();
+            else landed<(ST - 2) * NL>();
+            fetch((x + ST - 1) % ST);
+            if (mode[x] != 0)
+                step(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], mode[x] == 1 || !whole, sc[x],
+                     tile[x] * kTile);
         }
     }
-#pragma unroll
-    for (int x = 0; x < KB; ++x) {
-        const int j = w0 + 32 * x + (lane_id() & 31);
-        // dk and dv are contiguous (b, sk, hkv, d)
-        const int64_t at = ((static_cast<int64_t>(b) * a.sk + j) * a.hkv + kvh) * a.d;
-        store_rows<DP>(dk[x], a.scale, a.dk + at, j < a.sk, a.d);
-        store_rows<DP>(dv[x], 1.0f, a.dv + at, j < a.sk, a.d);
-    }
+done:
+    const Args z = again(a);
+    // dk and dv are contiguous (b, sk, hkv, d)
+    const int64_t to = ((static_cast<int64_t>(b) * z->sk + j) * z->hkv + kvh) * z->d;
+    store_rows<DP>(dk, z->scale, z->dk + to, j < z->sk, z->d);
+    store_rows<DP>(dv, 1.0f, z->dv + to, j < z->sk, z->d);
 }
 
 template <int DP, int MOD>
 void dq(const AttnArgs& a, hipStream_t stream) {
-    constexpr int QB = 1, NW = 4, BM = 32 * QB * NW;
+    constexpr int NW = 4, ST = DP == 128 ? 2 : 3, BM = 32 * NW;
     const int blocks = (a.sq + BM - 1) / BM * a.b * a.hq;
-    k_attn_dq<DP, QB, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    k_attn_dq<DP, NW, ST, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
 }
 template <int DP, int MOD>
 void dkv(const AttnArgs& a, hipStream_t stream) {
-    constexpr int KB = 1, NW = 4, BN = 32 * KB * NW;
+    constexpr int NW = 4, ST = 3, BN = 32 * NW;
     const int blocks = (a.sk + BN - 1) / BN * a.b * a.hkv;
-    k_attn_dkv<DP, KB, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    k_attn_dkv<DP, NW, ST, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
 }
 
 }  // namespace

@@ -11,7 +11,14 @@
 // from LDS in that order.
 #pragma once
 
+#include <type_traits>
+#include <utility>
+
 #include "lm_common.hpp"
+
+// LDS addresses are 32-bit integers on the device; the host pass of the
+// compiler, which runs none of this, sees them cast to 64-bit pointers.
+#pragma clang diagnostic ignored "-Wint-to-pointer-cast"
 
 namespace muon {
 namespace attn {
@@ -19,6 +26,16 @@ namespace attn {
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// The launch arguments where the launch left them.  A kernel that held them
+// all would run out of scalar registers inside its loop; again() makes a rare
+// path read them once more instead.
+typedef __attribute__((address_space(4))) const AttnArgs* Args;
+__device__ __forceinline__ Args arguments() { return (Args)__builtin_amdgcn_kernarg_segment_ptr(); }
+__device__ __forceinline__ Args again(Args a) {
+    asm volatile("" : "+s"(a));
+    return a;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -55,20 +72,97 @@ __device__ __forceinline__ auto rsrc(const void* p, uint32_t bytes) {
 // LDS tile of kTile rows of DP (head size padded to 64, 96 or 128) bf16.
 // Chunk c (16 bytes) of row r lies at slot c ^ f(r).  f makes 16 consecutive
 // rows of one chunk fall on distinct banks (operands read along the row, 16
-// bytes a lane) and 4 rows of one 64-byte piece too (transposing reads).  The
-// 192-byte rows of DP = 96 are padded to 208 bytes instead.
+// bytes a lane) and 4 rows of one 64-byte piece too (transposing reads).
 template <int DP>
 struct Tile {
     static constexpr int CPR = DP / 8;
-    static constexpr int LD = DP == 96 ? 104 : DP;
+    static constexpr int LD = DP;
     static constexpr int ELEMS = kTile * LD;
     __device__ static __forceinline__ int f(int r) {
         if constexpr (DP == 128) return ((r & 3) << 2) | ((r >> 2) & 3);
         else if constexpr (DP == 64) return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-        else return 0;
+        else return (r >> 2) & 3;  // 192-byte rows already step by 4 chunks
     }
     __device__ static __forceinline__ int at(int r, int c) { return r * LD + ((c ^ f(r)) << 3); }
 };
+
+// Byte address of LDS memory, as the direct loads take it.
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)(p)));
+}
+
+// Direct loads from memory to LDS: lane l's 16 (4) bytes land at lds + 16 l
+// (4 l).  In asm, because the compiler cannot tell which LDS reads such a
+// load in flight concerns and would wait for it before every one; the loads
+// have no result registers, and landed() orders them.
+__device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t voff, u32x4 desc) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
+                 : "memory");
+}
+__device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, u32x4 desc) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
+                 : "memory");
+}
+// All but this wave's last N loads have landed and its LDS reads are done,
+// and so for every wave of the workgroup.
+template <int N>
+__device__ __forceinline__ void landed() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ u32x4 descriptor(const void* p, uint32_t bytes) {
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a))),
+                 static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a >> 32))) & 0xffffu,
+                 static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(bytes))), 0x00027000u};
+}
+
+// Loads tiles of kTile rows straight into LDS, NT threads together.  Rows past
+// `rows` and values past the head size come as zeros, whatever memory holds
+// there.
+template <int DP, int NT>
+struct Direct {
+    static constexpr int N = kTile * Tile<DP>::CPR / NT;  // loads per thread
+    static_assert(N * NT == kTile * Tile<DP>::CPR, "whole chunks per thread");
+    // loads of whole multiples of 16 rows differ by a fixed step (the layout
+    // repeats): one offset is kept, and the others made from it
+    static constexpr bool kSteps = NT % Tile<DP>::CPR == 0 && NT / Tile<DP>::CPR % 16 == 0;
+    uint32_t voff[kSteps ? 1 : N];
+    const bf16_t* base;  // row 0 of the sequence
+    int64_t stride;      // elements per row
+    int rows;
+    uint32_t row_bytes;
+
+    __device__ __forceinline__ void init(const bf16_t* p, int64_t s, int nrows, int d) {
+        base = p;
+        stride = s;
+        rows = nrows;
+        row_bytes = 2 * d;
+#pragma unroll
+        for (int i = 0; i < (kSteps ? 1 : N); ++i) {
+            const int id = static_cast<int>(threadIdx.x) % NT + i * NT;
+            const int r = id / Tile<DP>::CPR, c = (id % Tile<DP>::CPR) ^ Tile<DP>::f(r);
+            voff[i] = 8 * c < d ? static_cast<uint32_t>(r) * static_cast<uint32_t>(2 * s) + 16 * c : 0x80000000u;
+        }
+    }
+    // row0 < rows; tile: byte address
+    __device__ __forceinline__ void load(int row0, uint32_t tile) const {
+        const int left = rows - row0 < kTile ? rows - row0 : kTile;
+        const u32x4 d = descriptor(base + static_cast<int64_t>(row0) * stride,
+                                   static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(2 * stride) + row_bytes);
+        const uint32_t lds = tile + wave_id() * 64 % NT * 16;
+        uint32_t v = voff[0];
+        asm volatile("" : "+v"(v));  // (the sums below are not kept in registers)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            load_lds16(lds + i * NT * 16, kSteps ? v + i * (NT / Tile<DP>::CPR) * static_cast<uint32_t>(2 * stride) : voff[kSteps ? 0 : i], d);
+    }
+};
+// One 4-byte value of each of kTile rows (row0 < rows), every wave loading all
+// of them (the waves' counts of loads stay equal).
+__device__ __forceinline__ void load_values(const void* p, int row0, int rows, uint32_t lds) {
+    const int left = rows - row0 < kTile ? rows - row0 : kTile;
+    load_lds4(lds, 4 * lane_id(), descriptor(static_cast<const char*>(p) + 4 * static_cast<int64_t>(row0), 4 * left));
+}
 
 // Moves one tile of kTile rows from memory through registers to LDS.  Rows
 // past `rows` and values past the head size come as zeros, whatever memory
@@ -112,18 +206,18 @@ struct Loader {
     }
 };
 
-// A operand read along the rows of a tile: rows 32 rb + lane % 32, columns 16
-// t + 8 half .. + 7.
+// A operand read along the rows of the tile at byte address `tile`: rows 32 rb
+// + lane % 32, columns 16 t + 8 half .. + 7.
 template <int DP>
 struct RowFrag {
-    int off[DP / 16];
+    uint32_t off[DP / 16];
     __device__ __forceinline__ void init() {
         const int r = lane_id() & 31, h = lane_id() >> 5;
 #pragma unroll
-        for (int t = 0; t < DP / 16; ++t) off[t] = Tile<DP>::at(r, 2 * t + h);
+        for (int t = 0; t < DP / 16; ++t) off[t] = 2 * Tile<DP>::at(r, 2 * t + h);
     }
-    __device__ __forceinline__ bf16x8 read(const bf16_t* tile, int rb, int t) const {
-        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(tile + 32 * rb * Tile<DP>::LD + off[t]));
+    __device__ __forceinline__ bf16x8 read(uint32_t tile, int rb, int t) const {
+        return __builtin_bit_cast(bf16x8, *(__attribute__((address_space(3))) const u32x4*)(off[t] + (tile + 64 * rb * Tile<DP>::LD)));
     }
 };
 
@@ -133,7 +227,7 @@ struct RowFrag {
 // values (k + r / 4, c + 4 (r % 4)) and lane i receives (k .. k + 3, c + i).
 template <int DP>
 struct ColFrag {
-    int off[DP / 32][2];
+    uint32_t off[DP / 32][2];
     __device__ __forceinline__ void init() {
         const int g = lane_id() >> 4, r = lane_id() & 15, h = g >> 1;
 #pragma unroll
@@ -142,17 +236,16 @@ struct ColFrag {
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * e + 4 * h + (r >> 2);
                 const int col = 32 * dt + 16 * (g & 1) + 4 * (r & 3);
-                off[dt][e] = Tile<DP>::at(row, col >> 3) + (col & 7);
+                off[dt][e] = 2 * (Tile<DP>::at(row, col >> 3) + (col & 7));
             }
     }
-    __device__ __forceinline__ bf16x8 read(const bf16_t* tile, int t, int dt) const {
-        const bf16_t* p = tile + 16 * t * Tile<DP>::LD;
-        const s16x4 lo = tr(p + off[dt][0]), hi = tr(p + off[dt][1]);
+    __device__ __forceinline__ bf16x8 read(uint32_t tile, int t, int dt) const {
+        const uint32_t at = tile + 32 * t * Tile<DP>::LD;
+        const s16x4 lo = tr(off[dt][0] + at), hi = tr(off[dt][1] + at);
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
     }
-    __device__ static __forceinline__ s16x4 tr(const bf16_t* p) {
-        return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<const s16x4*>(p)));
+    __device__ static __forceinline__ s16x4 tr(uint32_t at) {
+        return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
     }
 };
 
@@ -190,6 +283,32 @@ __device__ __forceinline__ void load_rows(bf16x8 (&f)[DP / 16], const bf16_t* ba
     }
 }
 
+// The values are in registers from here on (else the compiler waits for them
+// inside the loop that uses them, and with them for every direct load).
+template <int N>
+__device__ __forceinline__ void settle(bf16x8 (&f)[N]) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+        u32x4 v = __builtin_bit_cast(u32x4, f[t]);
+        asm volatile("" : "+v"(v));
+        f[t] = __builtin_bit_cast(bf16x8, v);
+    }
+}
+
+// f(integral_constant<int, I>) for I = A .. B - 1.
+template <int A, int... I, typename F>
+__device__ __forceinline__ void each_of(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, A + I>{}), ...);
+}
+template <int A, int B, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of<A>(f, std::make_integer_sequence<int, (B > A ? B - A : 0)>{});
+}
+
+// Nothing is scheduled across: keeps matrix instructions, the LDS reads of
+// later ones and the vector work between them in the order written.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 // Stores a transposed result (column l % 32 = a row of the output, rows = its
 // columns 32 dt ..): the halves swap pieces so that every lane stores 16
 // contiguous bytes.
@@ -222,53 +341,69 @@ struct Seq {
     int n;      // keys (and positions) below this one are real
     int start;  // position of query 0
     int pre;    // keys below this one are seen by every query
+    int b;
     const int32_t* doc;
 };
-__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b) {
+__device__ __forceinline__ Seq sequence(Args a, int b) {
     Seq s;
-    s.n = a.sk;
-    if (a.lengths) {
-        const int len = a.lengths[b];
-        s.n = len < 0 ? 0 : (len < a.sk ? len : a.sk);
+    s.b = b;
+    s.n = a->sk;
+    if (a->lengths) {
+        const int len = a->lengths[b];
+        s.n = len < 0 ? 0 : (len < a->sk ? len : a->sk);
     }
-    int st = a.sk - a.sq;
-    if (a.starts) st = a.starts[b];
+    int st = a->sk - a->sq;
+    if (a->starts) st = a->starts[b];
     s.start = st < -kMaxPos ? -kMaxPos : (st > kMaxPos ? kMaxPos : st);
     s.pre = 0;
-    if (a.prefix) {
-        const int p = a.prefix[b];
+    if (a->prefix) {
+        const int p = a->prefix[b];
         s.pre = p < 0 ? 0 : (p < s.n ? p : s.n);
     }
-    s.doc = a.documents ? a.documents + static_cast<int64_t>(b) * a.doc_b : nullptr;
+    s.doc = a->documents ? a->documents + static_cast<int64_t>(b) * a->doc_b : nullptr;
     return s;
 }
-__device__ __forceinline__ int doc_of(const Seq& s, const AttnArgs& a, int pos) {
-    const int p = pos < 0 ? 0 : (pos < a.sk ? pos : a.sk - 1);
+__device__ __forceinline__ int doc_of(const Seq& s, Args a, int pos) {
+    const int p = pos < 0 ? 0 : (pos < a->sk ? pos : a->sk - 1);
     return s.doc[p];
 }
 // A query's position is real: with lengths, positions past the length are
 // padding and see nothing.
-__device__ __forceinline__ bool real_row(const Seq& s, const AttnArgs& a, int pos) {
-    return a.lengths == nullptr || pos < s.n;
+__device__ __forceinline__ bool real_row(const Seq& s, Args a, int pos) {
+    return a->lengths == nullptr || pos < s.n;
 }
 
-// Keys one query sees outside the document rule: lo <= j <= hi, or j < pre.
+// One query: its position and document.  The keys it sees outside the
+// document rule are lo <= j <= hi, or j < pre.
 struct Row {
-    int pos, lo, hi, pre, doc;
+    int pos, doc;
 };
-__device__ __forceinline__ Row row_of(const Seq& s, const AttnArgs& a, int pos) {
-    Row r;
-    r.pos = pos;
-    r.lo = 0;
-    r.hi = s.n - 1;
-    r.pre = s.pre;
-    if (a.causal && pos < r.hi) r.hi = pos;
-    if (a.window) {
-        if (pos - a.window + 1 > r.lo) r.lo = pos - a.window + 1;
-        if (pos + a.window - 1 < r.hi) r.hi = pos + a.window - 1;
+__device__ __forceinline__ Row row_of(const Seq& s, Args a, int pos) {
+    return {pos, s.doc ? doc_of(s, a, pos) : 0};
+}
+// What hides keys from one query in the tile at k0, relative to the first key
+// of the lane's half: lo <= j <= lo + span (as one unsigned comparison) or j <
+// pre is seen.
+struct Hide {
+    int lo, span, pre, doc;
+    bool none;
+};
+__device__ __forceinline__ Hide hide_of(const Row& r, const Seq& s, Args a, int k0, int h4) {
+    a = again(a);
+    int lo = 0, hi = s.n - 1;
+    if (a->causal && r.pos < hi) hi = r.pos;
+    if (a->window) {
+        if (r.pos - a->window + 1 > lo) lo = r.pos - a->window + 1;
+        if (r.pos + a->window - 1 < hi) hi = r.pos + a->window - 1;
     }
-    r.doc = s.doc && a.sk > 0 ? doc_of(s, a, pos) : 0;
-    return r;
+    return {lo - k0 - h4, hi - lo, s.pre - k0 - h4, r.doc, hi < lo};
+}
+// j: the key relative to k0 + h4; sdoc: the documents of the half's keys, or null.
+__device__ __forceinline__ bool seen(const Hide& h, int j, const int* sdoc) {
+    bool vis = !h.none && static_cast<uint32_t>(j - h.lo) <= static_cast<uint32_t>(h.span);
+    vis = vis || j < h.pre;
+    if (sdoc) vis = vis && sdoc[j] == h.doc;
+    return vis;
 }
 
 // Whether a block of queries at positions [p0, p1] (documents in [d0, d1])
@@ -278,10 +413,10 @@ __device__ __forceinline__ Row row_of(const Seq& s, const AttnArgs& a, int pos) 
 struct Sight {
     bool some, all;
 };
-__device__ __forceinline__ Sight sight(const Seq& s, const AttnArgs& a, int p0, int p1, int d0, int d1, int j0, int j1,
+__device__ __forceinline__ Sight sight(const Seq& s, Args a, int p0, int p1, int d0, int d1, int j0, int j1,
                                        int e0, int e1) {
-    const bool span_some = (!a.causal || j0 <= p1) && (!a.window || (j1 > p0 - a.window && j0 < p1 + a.window));
-    const bool span_all = (!a.causal || j1 <= p0) && (!a.window || (p1 - j0 < a.window && j1 - p0 < a.window));
+    const bool span_some = (!a->causal || j0 <= p1) && (!a->window || (j1 > p0 - a->window && j0 < p1 + a->window));
+    const bool span_all = (!a->causal || j1 <= p0) && (!a->window || (p1 - j0 < a->window && j1 - p0 < a->window));
     Sight r;
     r.some = j0 <= j1 && (span_some || j0 < s.pre);
     r.all = span_all || j1 < s.pre;
@@ -294,7 +429,7 @@ __device__ __forceinline__ Sight sight(const Seq& s, const AttnArgs& a, int p0, 
 
 // Lowest and highest document of the positions [p0, p1] of a sequence, over
 // the wave.
-__device__ __forceinline__ void doc_range(const Seq& s, const AttnArgs& a, int p0, int p1, int& lo, int& hi) {
+__device__ __forceinline__ void doc_range(const Seq& s, Args a, int p0, int p1, int& lo, int& hi) {
     lo = 0x7fffffff;
     hi = static_cast<int>(0x80000000u);
     if (!s.doc) return;
@@ -317,11 +452,11 @@ __device__ __forceinline__ void doc_range(const Seq& s, const AttnArgs& a, int p
 struct Span {
     int p0, p1, d0, d1;
 };
-__device__ __forceinline__ Span query_span(const Seq& s, const AttnArgs& a, int i0, int i1) {
+__device__ __forceinline__ Span query_span(const Seq& s, Args a, int i0, int i1) {
     Span r;
     r.p0 = s.start + i0;
     r.p1 = s.start + i1 - 1;
-    if (a.lengths && r.p1 >= s.n) r.p1 = s.n - 1;
+    if (a->lengths && r.p1 >= s.n) r.p1 = s.n - 1;
     doc_range(s, a, r.p0, r.p1, r.d0, r.d1);
     return r;
 }
@@ -331,13 +466,13 @@ __device__ __forceinline__ Span query_span(const Seq& s, const AttnArgs& a, int 
 struct KeyTiles {
     uint64_t wg, some, all;
     int base, end;
-    __device__ __forceinline__ void fill(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
-                                         const int2* docs) {
+    __device__ __forceinline__ void fill(const Seq& s, Args a, const Span& g, const Span& w) {
+        a = again(a);
         const int t = base + lane_id(), j0 = t * kTile;
         int j1 = j0 + kTile - 1;
         if (j1 >= s.n) j1 = s.n - 1;
         int2 e = {0, 0};
-        if (s.doc && t < a.n_tiles) e = docs[t];
+        if (s.doc && t < a->n_tiles) e = a->doc_tiles[static_cast<int64_t>(s.b) * a->n_tiles + t];
         const bool in = t < end;
         const Sight x = sight(s, a, g.p0, g.p1, g.d0, g.d1, j0, j1, e.x, e.y);
         const Sight y = sight(s, a, w.p0, w.p1, w.d0, w.d1, j0, j1, e.x, e.y);
@@ -345,13 +480,12 @@ struct KeyTiles {
         some = __ballot(in && w.p0 <= w.p1 && y.some);
         all = __ballot(in && y.all && j0 + kTile <= s.n);
     }
-    __device__ __forceinline__ void init(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
-                                         const int2* docs) {
+    __device__ __forceinline__ void init(const Seq& s, Args a, const Span& g, const Span& w) {
         int lo = 0, hi = s.n - 1;
-        if (a.causal && g.p1 < hi) hi = g.p1;
-        if (a.window) {
-            if (g.p0 - a.window + 1 > lo) lo = g.p0 - a.window + 1;
-            if (g.p1 + a.window - 1 < hi) hi = g.p1 + a.window - 1;
+        if (a->causal && g.p1 < hi) hi = g.p1;
+        if (a->window) {
+            if (g.p0 - a->window + 1 > lo) lo = g.p0 - a->window + 1;
+            if (g.p1 + a->window - 1 < hi) hi = g.p1 + a->window - 1;
         }
         if (s.pre > 0) {
             lo = 0;
@@ -361,15 +495,14 @@ struct KeyTiles {
         base = lo / kTile;
         end = hi < 0 ? 0 : hi / kTile + 1;
         wg = some = all = 0;
-        if (base < end) fill(s, a, g, w, docs);
+        if (base < end) fill(s, a, g, w);
     }
     // Next tile, or -1.  mode: 0 this wave sees nothing of it, 1 some, 2 all.
-    __device__ __forceinline__ int next(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
-                                        const int2* docs, int& mode) {
+    __device__ __forceinline__ int next(const Seq& s, Args a, const Span& g, const Span& w, int& mode) {
         while (wg == 0) {
             base += 64;
             if (base >= end) return -1;
-            fill(s, a, g, w, docs);
+            fill(s, a, g, w);
         }
         const int i = __builtin_ctzll(wg);
         wg &= wg - 1;
@@ -379,22 +512,24 @@ struct KeyTiles {
 };
 
 // Queries that see one key: those at positions lo .. hi of its document.
-__device__ __forceinline__ Row col_of(const Seq& s, const AttnArgs& a, int j) {
-    Row r;
+struct Col {
+    int pos, lo, hi, doc;
+};
+__device__ __forceinline__ Col col_of(const Seq& s, Args a, int j) {
+    Col r;
     r.pos = j;
-    r.pre = 0;
     r.lo = s.start;
-    r.hi = s.start + a.sq - 1;
-    if (a.lengths && r.hi >= s.n) r.hi = s.n - 1;
+    r.hi = s.start + a->sq - 1;
+    if (a->lengths && r.hi >= s.n) r.hi = s.n - 1;
     if (j >= s.pre) {
-        if (a.causal && j > r.lo) r.lo = j;
-        if (a.window) {
-            if (j - a.window + 1 > r.lo) r.lo = j - a.window + 1;
-            if (j + a.window - 1 < r.hi) r.hi = j + a.window - 1;
+        if (a->causal && j > r.lo) r.lo = j;
+        if (a->window) {
+            if (j - a->window + 1 > r.lo) r.lo = j - a->window + 1;
+            if (j + a->window - 1 < r.hi) r.hi = j + a->window - 1;
         }
     }
     if (j >= s.n) r.hi = r.lo - 1;
-    r.doc = s.doc && a.sk > 0 ? doc_of(s, a, j) : 0;
+    r.doc = s.doc ? doc_of(s, a, j) : 0;
     return r;
 }
 
@@ -402,14 +537,15 @@ __device__ __forceinline__ Row col_of(const Seq& s, const AttnArgs& a, int j) {
 struct QueryTiles {
     uint64_t wg, some, all;
     int base, end, rows;
-    __device__ __forceinline__ void fill(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
-                                         const int2* docs) {
+    __device__ __forceinline__ void fill(const Seq& s, Args a, const Span& g, const Span& w) {
+        a = again(a);
         const int i0 = (base + lane_id()) * kTile;
         const int i1 = i0 + kTile < rows ? i0 + kTile : rows;
         const int p0 = s.start + i0, p1 = s.start + i1 - 1;
         int2 e = {0, 0};
         if (s.doc && i0 < rows) {
-            const int x = p0 < 0 ? 0 : (p0 < a.sk ? p0 : a.sk - 1), y = p1 < 0 ? 0 : (p1 < a.sk ? p1 : a.sk - 1);
+            const int x = p0 < 0 ? 0 : (p0 < a->sk ? p0 : a->sk - 1), y = p1 < 0 ? 0 : (p1 < a->sk ? p1 : a->sk - 1);
+            const int2* docs = a->doc_tiles + static_cast<int64_t>(s.b) * a->n_tiles;
             const int2 ex = docs[x / kTile], ey = docs[y / kTile];
             e = {ex.x < ey.x ? ex.x : ey.x, ex.y > ey.y ? ex.y : ey.y};
         }
@@ -421,30 +557,28 @@ struct QueryTiles {
         all = __ballot(in && y.all && i0 + kTile <= rows);
     }
     // rows: queries that are real
-    __device__ __forceinline__ void init(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
-                                         const int2* docs) {
-        rows = a.sq;
-        if (a.lengths && s.n - s.start < rows) rows = s.n - s.start;
+    __device__ __forceinline__ void init(const Seq& s, Args a, const Span& g, const Span& w) {
+        rows = a->sq;
+        if (a->lengths && s.n - s.start < rows) rows = s.n - s.start;
         int lo = 0, hi = rows - 1;
         if (g.p0 >= s.pre) {
-            if (a.causal && g.p0 - s.start > lo) lo = g.p0 - s.start;
-            if (a.window) {
-                if (g.p0 - a.window + 1 - s.start > lo) lo = g.p0 - a.window + 1 - s.start;
-                if (g.p1 + a.window - 1 - s.start < hi) hi = g.p1 + a.window - 1 - s.start;
+            if (a->causal && g.p0 - s.start > lo) lo = g.p0 - s.start;
+            if (a->window) {
+                if (g.p0 - a->window + 1 - s.start > lo) lo = g.p0 - a->window + 1 - s.start;
+                if (g.p1 + a->window - 1 - s.start < hi) hi = g.p1 + a->window - 1 - s.start;
             }
         }
         if (g.p0 > g.p1) hi = -1;
         base = lo / kTile;
         end = hi < 0 ? 0 : hi / kTile + 1;
         wg = some = all = 0;
-        if (base < end) fill(s, a, g, w, docs);
+        if (base < end) fill(s, a, g, w);
     }
-    __device__ __forceinline__ int next(const Seq& s, const AttnArgs& a, const Span& g, const Span& w,
-                                        const int2* docs, int& mode) {
+    __device__ __forceinline__ int next(const Seq& s, Args a, const Span& g, const Span& w, int& mode) {
         while (wg == 0) {
             base += 64;
             if (base >= end) return -1;
-            fill(s, a, g, w, docs);
+            fill(s, a, g, w);
         }
         const int i = __builtin_ctzll(wg);
         wg &= wg - 1;
@@ -463,11 +597,11 @@ struct Score {
     float slope;  // slope * log2e
 };
 template <int MOD>
-__device__ __forceinline__ Score score_of(const AttnArgs& a, int head) {
+__device__ __forceinline__ Score score_of(Args a, int head) {
     Score s;
-    s.a = a.softcap * kLog2e;
-    s.c = (MOD & kCap) ? 2.0f * a.scale * kLog2e / a.softcap : a.scale * kLog2e;
-    s.slope = (MOD & kBias) ? a.slopes[head] * kLog2e : 0.0f;
+    s.a = a->softcap * kLog2e;
+    s.c = (MOD & kCap) ? 2.0f * a->scale * kLog2e / a->softcap : a->scale * kLog2e;
+    s.slope = (MOD & kBias) ? a->slopes[head] * kLog2e : 0.0f;
     return s;
 }
 // dist: |query position - key|.  r receives 1 / (exp(2 y) + 1).

@@ -83,7 +83,7 @@ int check_rows(const char* name, const void* p, const int64_t* strides, int64_t 
 struct AttnPlan {
     bool split;
     int splits, chunk;
-    size_t off_docs, off_part, off_delta, bytes;
+    size_t off_docs, off_part, off_stats, bytes;
 };
 
 // Few rows per key head (a step of generation), or too few workgroups of
@@ -118,8 +118,8 @@ AttnPlan plan_backward(const muon_attention_args* x) {
     size_t at = 0;
     p.off_docs = at;
     if (x->documents) at = align256(at + static_cast<size_t>(x->batch) * tiles * sizeof(int2));
-    p.off_delta = at;
-    at = align256(at + static_cast<size_t>(x->batch) * x->heads * x->sq * sizeof(float));
+    p.off_stats = at;
+    at = align256(at + static_cast<size_t>(x->batch) * x->heads * x->sq * 2 * sizeof(float));
     p.bytes = at > 256 ? at : 256;
     return p;
 }
@@ -156,7 +156,8 @@ AttnArgs attn_args(const muon_attention_args* x, const AttnPlan& p, void* ws) {
     char* w = static_cast<char*>(ws);
     a.doc_tiles = reinterpret_cast<int2*>(w + p.off_docs);
     a.part = reinterpret_cast<float*>(w + p.off_part);
-    a.delta = reinterpret_cast<float*>(w + p.off_delta);
+    a.stats = reinterpret_cast<float*>(w + p.off_stats);
+    a.delta_at = x->batch * x->heads * x->sq;
     a.b = static_cast<int>(x->batch);
     a.sq = static_cast<int>(x->sq);
     a.sk = static_cast<int>(x->sk);

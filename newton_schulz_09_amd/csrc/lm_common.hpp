@@ -20,7 +20,9 @@ constexpr int kTile = 64;
 struct AttnArgs {
     const bf16_t *q, *k, *v, *dout;
     bf16_t *out, *dq, *dk, *dv;
-    float *lse, *delta;
+    float *lse;
+    float* stats;       // backward: lse terms, then -delta, delta_at floats on
+    int64_t delta_at;
     int64_t q_b, q_s, q_h, k_b, k_s, k_h, v_b, v_s, v_h, do_b, do_s, do_h, o_b, o_s, o_h;
     int64_t doc_b;
     const float* slopes;
