@@ -197,7 +197,10 @@ def attention_backward(dout, q, k, v, out, lse, scale=None, causal=True, window=
     """Gradients ``(dq, dk, dv)`` (bfloat16, contiguous) from ``dout``, the
     gradient of ``out``, and the arguments and results of ``attention``.  The
     gradients of a shared key head sum over its query heads."""
-    dev = q.device if isinstance(q, torch.Tensor) else torch.device("cpu")
+    for t, name in ((q, "q"), (k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    dev = q.device
     _tensor(dout, "dout", _BF16, dev, 4)
     _last(dout, "dout")
     if out is None or lse is None:
