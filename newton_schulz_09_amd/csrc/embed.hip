@@ -3,10 +3,10 @@
 // the order of i in float32, without atomics on floating values.
 //
 // Both are bound by memory.  The gradient sorts the tokens first (k_embed_sort,
-// stable), then sums windows of kEmbedWindow sorted entries (k_embed_sum), so
-// that a token's work is spread over many workgroups however often it occurs,
-// and last joins the runs that cross windows and writes the rows of tokens
-// that do not occur (k_embed_rest).
+// stable), then sums windows of sorted entries and writes the rows of tokens
+// that do not occur (k_embed_sum), so that a token's work is spread over many
+// workgroups however often it occurs, and last joins the runs that cross
+// windows (k_embed_join).
 #include "../../include/muon.h"
 #include "lm_common.hpp"
 
@@ -15,12 +15,20 @@ namespace muon {
 namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 template <typename T, int V>
 __device__ __forceinline__ void load_e(const T* p, float (&x)[V]) {
     if constexpr (V == 1) {
         if constexpr (sizeof(T) == 2) x[0] = bf16_to_f32(p[0]);
         else x[0] = p[0];
+    } else if constexpr (sizeof(T) == 2 && V == 4) {
+        const u32x2 u = *reinterpret_cast<const u32x2*>(p);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
     } else if constexpr (sizeof(T) == 2) {
         const u32x4 u = *reinterpret_cast<const u32x4*>(p);
 #pragma unroll
@@ -28,6 +36,10 @@ __device__ __forceinline__ void load_e(const T* p, float (&x)[V]) {
             x[2 * i] = __uint_as_float(u[i] << 16);
             x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
         }
+    } else if constexpr (V == 4) {
+        const f32x4 u = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = u[i];
     } else {
         const f32x4 u = reinterpret_cast<const f32x4*>(p)[0], v = reinterpret_cast<const f32x4*>(p)[1];
 #pragma unroll
@@ -42,13 +54,16 @@ __device__ __forceinline__ void store_e(T* p, const float (&x)[V]) {
     if constexpr (V == 1) {
         if constexpr (sizeof(T) == 2) p[0] = f32_to_bf16(x[0]);
         else p[0] = x[0];
+    } else if constexpr (sizeof(T) == 2 && V == 4) {
+        const u32x2 u = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3])};
+        __builtin_nontemporal_store(u, reinterpret_cast<u32x2*>(p));
     } else if constexpr (sizeof(T) == 2) {
         const u32x4 u = {f32x2_to_bf16x2(x[0], x[1]), f32x2_to_bf16x2(x[2], x[3]), f32x2_to_bf16x2(x[4], x[5]),
                          f32x2_to_bf16x2(x[6], x[7])};
         __builtin_nontemporal_store(u, reinterpret_cast<u32x4*>(p));
     } else {
         __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]}, reinterpret_cast<f32x4*>(p));
-        __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4*>(p) + 1);
+        if constexpr (V == 8) __builtin_nontemporal_store(f32x4{x[4], x[5], x[6], x[7]}, reinterpret_cast<f32x4*>(p) + 1);
     }
 }
 
@@ -82,39 +97,64 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a, int lanes) {
 }
 
 // Stable sort of the tokens: workgroup g owns the `span` table rows from g
-// span.  Its 16 waves take 16 consecutive parts of the tokens; a first pass
-// counts (per wave and row, and the tokens of lower rows, which is where the
-// workgroup's entries begin), a second one places.  No workgroup waits for
-// another one.  Every workgroup reads all the tokens from the caches: 65536
-// of them are 512 KiB.
+// span.  Its 16 waves take 16 consecutive parts of the tokens and look through
+// them once: they count (per wave and row, and the tokens of lower rows, which
+// is where the workgroup's entries begin) and list their own in LDS; then they
+// place the listed ones.  A wave whose list is full (a table of few rows, or
+// one token everywhere) looks through its part again instead.  No workgroup
+// waits for another one.  Every workgroup reads all the tokens from the
+// caches: 65536 of them are 512 KiB.
 constexpr int kSortWaves = 16;
-constexpr int kSortSpan = 512;  // table rows per workgroup at most
+constexpr int kSortSpan = 512;   // table rows per workgroup at most
+constexpr int kSortList = 1024;  // entries a wave can list
 __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const EmbedArgs a, int span) {
     __shared__ int32_t cnt[kSortWaves][kSortSpan];
+    __shared__ uint32_t list[kSortWaves][kSortList];  // place in the part * kSortSpan + row
     __shared__ int32_t below[kSortWaves];
     __shared__ int32_t wsum[kSortWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t lo = static_cast<int64_t>(blockIdx.x) * span;
-    const int rows = static_cast<int>(lo + span <= a.vocab ? span : a.vocab - lo);
+    const uint32_t base32 = static_cast<uint32_t>(lo);  // vocab is below 2^31
+    const uint32_t rows = static_cast<uint32_t>(lo + span <= a.vocab ? span : a.vocab - lo);
     for (int i = threadIdx.x; i < kSortWaves * kSortSpan; i += blockDim.x) (&cnt[0][0])[i] = 0;
     __syncthreads();
     const int64_t part = ((a.n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
     const int64_t i0 = wave * part, i1 = i0 + part < a.n ? i0 + part : a.n;
     constexpr int U = 8;
-    int32_t low = 0;
-    for (int64_t i = i0; i < i1; i += 64 * U) {
-        int64_t t[U];
+    // f(place, token relative to lo, mine) for the part's tokens, 64 at a time
+    auto walk = [&](auto&& f) {
+        for (int64_t i = i0; i < i1; i += 64 * U) {
+            uint32_t t[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) t[k] = i + 64 * k + lane < i1 ? token_at(a, i + 64 * k + lane) : -1;
+            for (int k = 0; k < U; ++k) {
+                t[k] = 0xffffffffu;  // outside the table
+                const int64_t at = i + 64 * k + lane;
+                if (at < i1) {
+                    if (a.tokens64) {
+                        const u32x2 w = static_cast<const u32x2*>(a.tokens)[at];
+                        t[k] = w.y == 0 ? w.x : 0xffffffffu;
+                    } else {
+                        t[k] = static_cast<const uint32_t*>(a.tokens)[at];
+                    }
+                }
+            }
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            low += t[k] >= 0 && t[k] < lo;
-            const int64_t x = t[k] - lo;
-            if (t[k] >= 0 && x >= 0 && x < rows) atomicAdd(&cnt[wave][x], 1);
+            for (int k = 0; k < U; ++k) f(i + 64 * k + lane, t[k]);
         }
-    }
-#pragma unroll
-    for (int m = 32; m; m >>= 1) low += __shfl_xor(low, m);
+    };
+    int32_t low = 0, listed = 0;
+    walk([&](int64_t i, uint32_t t) {
+        low += __popcll(__ballot(t < base32));
+        const bool mine = t - base32 < rows;
+        const uint64_t all = __ballot(mine);
+        if (all == 0) return;
+        if (mine) {
+            atomicAdd(&cnt[wave][t - base32], 1);
+            const int at = listed + __popcll(all & ((1ull << lane) - 1));
+            if (at < kSortList) list[wave][at] = static_cast<uint32_t>(i - i0) * kSortSpan + (t - base32);
+        }
+        listed += __popcll(all);
+    });
     if (lane == 0) below[wave] = low;
     __syncthreads();
     // thread x < kSortSpan: row x's entries per wave -> where they begin
@@ -142,68 +182,79 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const EmbedArgs 
     if (x < kSortSpan) {
 #pragma unroll
         for (int w = 0; w < kSortWaves; ++w) cnt[w][x] += first;
-        if (x < rows) a.offset[lo + x] = first;
-        if (x == rows - 1 && lo + rows == a.vocab) a.offset[a.vocab] = first + total;
+        if (x < static_cast<int>(rows)) a.offset[lo + x] = first;
+        if (x == static_cast<int>(rows) - 1 && lo + rows == a.vocab) a.offset[a.vocab] = first + total;
     }
     __syncthreads();
-    for (int64_t i = i0; i < i1; i += 64 * U) {
-        int64_t t[U];
-#pragma unroll
-        for (int k = 0; k < U; ++k) t[k] = i + 64 * k + lane < i1 ? token_at(a, i + 64 * k + lane) : -1;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            const int64_t y = t[k] - lo;
-            const bool mine = t[k] >= 0 && y >= 0 && y < rows;
-            uint64_t left = __ballot(mine);
-            while (left) {
-                // the lanes that hold the first one's token take places in order
-                const int lead = __builtin_ctzll(left);
-                const int32_t who = __shfl(static_cast<int32_t>(y), lead);
-                const bool same = mine && static_cast<int32_t>(y) == who;
-                const uint64_t all = __ballot(same);
-                const int32_t at = cnt[wave][who];
-                if (same) {
-                    const int32_t p = at + __popcll(all & ((1ull << lane) - 1));
-                    a.perm[p] = static_cast<int32_t>(i + 64 * k + lane);
-                    a.ids[p] = static_cast<int32_t>(t[k]);
-                }
-                if (lane == lead) cnt[wave][who] = at + __popcll(all);
-                __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-                __builtin_amdgcn_wave_barrier();
-                left &= ~all;
+    // the lanes that hold the first one's row take places in order, and so on
+    auto place = [&](int64_t i, int32_t y, bool mine) {
+        uint64_t left = __ballot(mine);
+        while (left) {
+            const int lead = __builtin_ctzll(left);
+            const int32_t who = __builtin_amdgcn_readlane(y, lead);
+            const bool same = mine && y == who;
+            const uint64_t all = __ballot(same);
+            const int32_t at = cnt[wave][who];
+            if (same) {
+                const int32_t p = at + __popcll(all & ((1ull << lane) - 1));
+                a.perm[p] = static_cast<int32_t>(i);
+                a.ids[p] = static_cast<int32_t>(lo) + y;
             }
+            if (lane == lead) cnt[wave][who] = at + __popcll(all);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            left &= ~all;
         }
+    };
+    if (listed <= kSortList && part <= (int64_t{1} << 32) / kSortSpan) {
+        for (int e = 0; e < listed; e += 64) {
+            const bool mine = e + lane < listed;
+            const uint32_t u = mine ? list[wave][e + lane] : 0;
+            place(i0 + u / kSortSpan, static_cast<int32_t>(u % kSortSpan), mine);
+        }
+    } else {
+        walk([&](int64_t i, uint32_t t) { place(i, static_cast<int32_t>(t - base32), t - base32 < rows); });
     }
 }
 
-// Sums of the runs of equal tokens of one window.  A run inside the window is
-// written as the table's row; the first run goes to part row 2 w and the last
-// to 2 w + 1 where they cross the window's border.
+// The first workgroups: sums of the runs of equal tokens of one window.  A run
+// inside the window is written as the table's row; where the first and the
+// last run cross the window's border, their sums go to part rows 2 w and
+// 2 w + 1.  The workgroups after them write the rows of tokens that do not
+// occur, kZeroRows of the table each (in one launch, because the sums wait
+// for memory and the zeros do not).
+constexpr int kZeroRows = 32;
+constexpr int kMaxWindow = 32;
 template <typename TS, typename TD, int V>
-__global__ __launch_bounds__(256) void k_embed_sum(const EmbedArgs a) {
-    __shared__ int32_t s_perm[kEmbedWindow], s_ids[kEmbedWindow + 2];
-    const int64_t total = a.offset[a.vocab], w0 = static_cast<int64_t>(blockIdx.x) * kEmbedWindow;
+__global__ __launch_bounds__(256) void k_embed_sum(const EmbedArgs a, int windows) {
+    __shared__ int32_t s_perm[kMaxWindow], s_ids[kMaxWindow + 2], s_off[kZeroRows + 1];
+    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
+    float acc[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+    if (static_cast<int>(blockIdx.x) >= windows) {
+        const int64_t r0 = static_cast<int64_t>(blockIdx.x - windows) * kZeroRows;
+        const int rows = a.vocab - r0 < kZeroRows ? static_cast<int>(a.vocab - r0) : kZeroRows;
+        if (static_cast<int>(threadIdx.x) <= rows) s_off[threadIdx.x] = a.offset[r0 + threadIdx.x];
+        __syncthreads();
+        if (c >= a.width) return;
+        for (int r = 0; r < rows; ++r)
+            if (s_off[r] == s_off[r + 1]) store_e<TD, V>(static_cast<TD*>(a.dst) + (r0 + r) * a.width + c, acc);
+        return;
+    }
+    const int64_t total = a.offset[a.vocab], w0 = static_cast<int64_t>(blockIdx.x) * a.window;
     if (w0 >= total) return;
-    const int n = total - w0 < kEmbedWindow ? static_cast<int>(total - w0) : kEmbedWindow;
-    if (threadIdx.x < kEmbedWindow + 2) {
+    const int n = total - w0 < a.window ? static_cast<int>(total - w0) : a.window;
+    if (static_cast<int>(threadIdx.x) < n + 2) {
         // with the neighbours on either side (-1: none)
         const int64_t i = w0 + threadIdx.x - 1;
         const bool in = i >= 0 && i < total;
         s_ids[threadIdx.x] = in ? a.ids[i] : -1;
         if (threadIdx.x >= 1 && static_cast<int>(threadIdx.x) <= n) s_perm[threadIdx.x - 1] = a.perm[i];
     }
-    if (blockDim.x < kEmbedWindow + 2 && threadIdx.x < 2) {  // a workgroup of one wave: the last two
-        const int64_t i = w0 + kEmbedWindow + threadIdx.x - 1;
-        s_ids[kEmbedWindow + threadIdx.x] = i < total ? a.ids[i] : -1;
-        if (kEmbedWindow - 1 + static_cast<int>(threadIdx.x) < n && threadIdx.x == 0) s_perm[kEmbedWindow - 1] = a.perm[i];
-    }
     __syncthreads();
-    const int c = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     if (c >= a.width) return;
     const TS* src = static_cast<const TS*>(a.src) + c;
-    float acc[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
     bool crosses = s_ids[0] == s_ids[1];  // the current run began before the window
     constexpr int U = 8;
     for (int e0 = 0; e0 < n; e0 += U) {
@@ -243,33 +294,48 @@ __global__ __launch_bounds__(256) void k_embed_sum(const EmbedArgs a) {
     }
 }
 
-// Rows of tokens that do not occur (zeros) and of those whose run crosses
-// windows (the sum of its parts in their order).
+// The run that begins in window blockIdx.x and goes on after it: the sum of its
+// parts, every fourth by each wave, the waves' sums joined in their order.
 template <typename TD, int V>
-__global__ __launch_bounds__(256) void k_embed_rest(const EmbedArgs a, int lanes) {
-    const int l = threadIdx.x % lanes, per = 256 / lanes;
-    const int64_t t = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes;
-    if (t >= a.vocab) return;
-    const int64_t first = a.offset[t], end = a.offset[t + 1];
-    const int64_t w0 = first / kEmbedWindow, w1 = (end - 1) / kEmbedWindow;
-    if (end > first && w0 == w1) return;
-    TD* dst = static_cast<TD*>(a.dst) + t * a.width;
-    const int pieces = a.width / V;
-    for (int c = l; c < pieces; c += lanes) {
-        float acc[V];
+__global__ __launch_bounds__(256) void k_embed_join(const EmbedArgs a) {
+    __shared__ float s[3][64][V];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t total = a.offset[a.vocab], w = blockIdx.x, next = (w + 1) * a.window;
+    if (next >= total) return;
+    const int t = a.ids[next - 1];
+    if (a.ids[next] != t) return;
+    const int64_t first = a.offset[t], w1 = (static_cast<int64_t>(a.offset[t + 1]) - 1) / a.window;
+    if (first < w * a.window) return;
+    const int c = (blockIdx.y * 64 + lane) * V;
+    const bool in = c < a.width;
+    // part rows of the run: 2 w + 1, then 2 (w + 1), 2 (w + 2), ...
+    float acc[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-        if (end > first) {
-            for (int64_t w = w0; w <= w1; ++w) {
-                const float* p = a.part + (2 * w + (w == w0 ? 1 : 0)) * a.width + c * V;
+    for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+    if (in) {
+        constexpr int U = 8;
+        for (int64_t x0 = w + wave; x0 <= w1; x0 += 4 * U) {
+            float x[U][V];
 #pragma unroll
-                for (int k = 0; k < V; ++k) acc[k] += p[k];
+            for (int u = 0; u < U; ++u) {
+                const int64_t x1 = x0 + 4 * u <= w1 ? x0 + 4 * u : w1;
+                load_e<float, V>(a.part + (2 * x1 + (x1 == w ? 1 : 0)) * a.width + c, x[u]);
             }
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] *= a.scale;
+            for (int u = 0; u < U; ++u)
+                if (x0 + 4 * u <= w1)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] += x[u][k];
         }
-        store_e<TD, V>(dst + c * V, acc);
     }
+    if (wave > 0)
+#pragma unroll
+        for (int k = 0; k < V; ++k) s[wave - 1][lane][k] = acc[k];
+    __syncthreads();
+    if (wave > 0 || !in) return;
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = (((acc[k] + s[0][lane][k]) + s[1][lane][k]) + s[2][lane][k]) * a.scale;
+    store_e<TD, V>(static_cast<TD*>(a.dst) + static_cast<int64_t>(t) * a.width + c, acc);
 }
 
 int row_lanes(int pieces) {
@@ -290,16 +356,17 @@ void bwd(const EmbedArgs& a, hipStream_t stream) {
     int64_t span = (a.vocab + 255) / 256;
     if (span > kSortSpan) span = kSortSpan;
     k_embed_sort<<<static_cast<uint32_t>((a.vocab + span - 1) / span), 64 * kSortWaves, 0, stream>>>(a, static_cast<int>(span));
-    if (a.n > 0) {
-        const int pieces = a.width / V;
-        int threads = (pieces + 63) / 64 * 64;
-        if (threads > 256) threads = 256;
-        k_embed_sum<TS, TD, V><<<dim3(static_cast<uint32_t>((a.n + kEmbedWindow - 1) / kEmbedWindow),
-                                      static_cast<uint32_t>((pieces + threads - 1) / threads)),
-                                 threads, 0, stream>>>(a);
-    }
-    const int lanes = row_lanes(a.width / V), per = 256 / lanes;
-    k_embed_rest<TD, V><<<static_cast<uint32_t>((a.vocab + per - 1) / per), 256, 0, stream>>>(a, lanes);
+    // pieces whose stores are contiguous over a wave
+    constexpr int W = V == 1 ? 1 : (sizeof(TS) == 2 && sizeof(TD) == 2 ? 8 : 4), J = V == 1 ? 1 : 4;
+    const int pieces = a.width / W;
+    int threads = (pieces + 63) / 64 * 64;
+    if (threads > 256) threads = 256;
+    const int64_t windows = (a.n + a.window - 1) / a.window, zeros = (a.vocab + kZeroRows - 1) / kZeroRows;
+    k_embed_sum<TS, TD, W><<<dim3(static_cast<uint32_t>(windows + zeros), static_cast<uint32_t>((pieces + threads - 1) / threads)),
+                             threads, 0, stream>>>(a, static_cast<int>(windows));
+    if (windows > 1)
+        k_embed_join<TD, J><<<dim3(static_cast<uint32_t>(windows - 1), static_cast<uint32_t>((a.width / J + 63) / 64)), 256, 0,
+                              stream>>>(a);
 }
 
 // fn<source, target, values a piece>

@@ -193,15 +193,40 @@ int check_qk(const muon_qk_norm_rope_args* x) {
         return refuse(MUON_ERR_UNSUPPORTED, "head size %lld is not even and up to %d", (long long)x->d, MUON_QK_NORM_MAX_D);
     if (!(x->eps >= 0.0) || !isfinite(static_cast<float>(x->eps)))
         return refuse(MUON_ERR_INVALID_ARG, "eps must be >= 0 and finite");
-    if (x->batch >= kMaxSeq || x->s >= kMaxSeq || x->heads[0] >= (1 << 20) || x->heads[1] >= (1 << 20) ||
+    if (x->batch >= kMaxSeq || x->s >= kMaxSeq || x->heads[0] >= (1 << 15) || x->heads[1] >= (1 << 15) ||
         x->limit > kMaxBlocks)
         return refuse(MUON_ERR_UNSUPPORTED, "too many rows");
     return MUON_OK;
 }
 
-int qk_blocks(const muon_qk_norm_rope_args* x, bool backward) {
-    const int64_t n = div_up(x->batch * x->s, 4), most = backward ? kQkMaxBlocks : 1 << 20;
-    return static_cast<int>(n < most ? n : most);
+struct QkPlan {
+    bool vector;
+    int lanes, chunk, runs_q, runs, blocks;
+};
+
+// A group of lanes takes one token and a run of its heads, so the token's
+// angles are loaded once for all of them; the runs are halved until the chip
+// has 8 waves per CU to work on (32 tokens of 40 float32 heads of 128: one
+// head per group).  The backward pass, whose workgroups leave a row of weight
+// gradients each, takes about 4 workgroups per CU and walks the tokens.
+QkPlan plan_qk(const muon_qk_norm_rope_args* x, bool vector, bool backward) {
+    QkPlan p{};
+    p.vector = vector;
+    const int v = vector ? (x->dtype == MUON_BF16 ? 8 : 4) : 1;
+    p.lanes = 1;
+    while (p.lanes < 64 && p.lanes * v < x->d / 2) p.lanes <<= 1;
+    const int64_t tokens = x->batch * x->s, groups = 256 / p.lanes, blocks = div_up(tokens, groups);
+    const int64_t most = x->heads[0] > x->heads[1] ? x->heads[0] : x->heads[1];
+    int64_t chunk = most > 0 ? most : 1;
+    auto runs = [&](int64_t heads) { return div_up(heads, chunk); };
+    while (chunk > 1 && blocks * (runs(x->heads[0]) + runs(x->heads[1])) < 512) chunk = div_up(chunk, 2);
+    p.chunk = static_cast<int>(chunk);
+    p.runs_q = static_cast<int>(runs(x->heads[0]));
+    p.runs = p.runs_q + static_cast<int>(runs(x->heads[1]));
+    int64_t limit = 1 << 20;
+    if (backward) limit = p.runs > 0 && p.runs < 1024 ? 1024 / p.runs : 1;
+    p.blocks = static_cast<int>(blocks < 1 ? 1 : (blocks < limit ? blocks : limit));
+    return p;
 }
 
 int run_qk(const muon_qk_norm_rope_args* x, bool backward, void* ws, size_t ws_bytes, hipStream_t stream) {
@@ -253,8 +278,11 @@ int run_qk(const muon_qk_norm_rope_args* x, bool backward, void* ws, size_t ws_b
     a.d = static_cast<int>(x->d);
     a.limit = static_cast<int>(x->limit);
     a.type = static_cast<int>(x->dtype);
-    a.blocks = qk_blocks(x, backward);
-    if (a.blocks < 1) a.blocks = 1;  // no rows: the weight gradients are zero
+    const QkPlan p = plan_qk(x, vec, backward);
+    a.lanes = p.lanes;
+    a.chunk = p.chunk;
+    a.runs_q = p.runs_q;
+    a.blocks = p.blocks;
     a.vector = vec;
     a.eps = static_cast<float>(x->eps);
     if (!any) a.b = 0;
@@ -272,6 +300,13 @@ bool embed_sizes_ok(int64_t n, int64_t vocab, int64_t width) {
     return n >= 0 && vocab > 0 && width > 0 && n < kMaxBlocks && vocab < kMaxBlocks && width <= (1 << 20) &&
            times(n, width) >= 0 && times(vocab, width) >= 0;
 }
+// 8 entries for a few tokens (one batch of loads), 32 for many: longer windows
+// leave fewer sums to join, shorter ones keep more of the chip busy.
+int embed_window(int64_t n) {
+    int w = 8;
+    while (w < 32 && n / (2 * w) >= 512) w *= 2;
+    return w;
+}
 EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t width) {
     EmbedPlan p{};
     size_t at = 0;
@@ -282,7 +317,7 @@ EmbedPlan embed_plan(int64_t n, int64_t vocab, int64_t width) {
     p.off_offset = at;
     at = align256(at + (static_cast<size_t>(vocab) + 1) * 4);
     p.off_part = at;
-    at = align256(at + static_cast<size_t>(div_up(n, kEmbedWindow)) * 2 * width * sizeof(float));
+    at = align256(at + static_cast<size_t>(div_up(n, embed_window(n))) * 2 * width * sizeof(float));
     p.bytes = at;
     return p;
 }
@@ -384,9 +419,15 @@ int muon_attention_backward(const muon_attention_args* x, void* ws, size_t ws_by
 size_t muon_qk_norm_rope_backward_workspace_size(const muon_qk_norm_rope_args* x) {
     using namespace muon;
     if (check_qk(x)) return 0;
-    const size_t n = align256(static_cast<size_t>(qk_blocks(x, true)) * 2 * x->d * sizeof(float));
-    const size_t least = align256(static_cast<size_t>(2 * x->d) * sizeof(float));
-    return n > least ? n : least;
+    // a row of sums per workgroup; the pointers' alignment, which decides
+    // between the two plans, is not looked at here
+    size_t n = 256;
+    for (const bool vector : {false, true}) {
+        const QkPlan p = plan_qk(x, vector, true);
+        const size_t bytes = align256(static_cast<size_t>(p.blocks) * p.runs * x->d * sizeof(float));
+        if (bytes > n) n = bytes;
+    }
+    return n;
 }
 
 int muon_qk_norm_rope(const muon_qk_norm_rope_args* x, void* stream) {
@@ -427,6 +468,7 @@ int muon_embedding_backward(const void* tokens, int token_bytes, const void* dou
     a.ids = reinterpret_cast<int32_t*>(w + p.off_ids);
     a.offset = reinterpret_cast<int32_t*>(w + p.off_offset);
     a.part = reinterpret_cast<float*>(w + p.off_part);
+    a.window = embed_window(n);
     const int st = launched(launch_embed_bwd(a, static_cast<hipStream_t>(stream)), "gradient of the embedding");
     return st ? st : done();
 }

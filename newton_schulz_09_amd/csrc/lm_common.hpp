@@ -57,10 +57,11 @@ struct QkArgs {
     const int32_t* positions;  // (b, s), or null: 0 .. s - 1
     float* part;             // weight gradients of every workgroup
     int b, s, d, limit, type;
+    int lanes;         // lanes that hold one head: a power of two
+    int chunk, runs_q;  // heads per workgroup; runs of so many query heads (the keys' follow)
     int blocks, vector;
     float eps;
 };
-constexpr int kQkMaxBlocks = 1024;
 hipError_t launch_qk_norm(const QkArgs& a, hipStream_t stream);
 hipError_t launch_qk_norm_bwd(const QkArgs& a, hipStream_t stream);
 
@@ -76,11 +77,11 @@ struct EmbedArgs {
     int vector;          // rows of whole aligned 16-byte pieces
     float scale;
     int32_t *perm, *ids, *offset;  // backward: sorted order, its tokens, first place of each token
-    float* part;                   // backward: sums of runs that cross windows
+    // backward: sorted entries per window, and the sums of its first and last
+    // run where they cross its border (rows 2 w, 2 w + 1)
+    int window;
+    float* part;
 };
-// Sorted entries per window of the backward pass; each window has two rows of
-// `part` (its first and its last run).
-constexpr int kEmbedWindow = 64;
 hipError_t launch_embed(const EmbedArgs& a, hipStream_t stream);
 hipError_t launch_embed_bwd(const EmbedArgs& a, hipStream_t stream);
 
