@@ -331,35 +331,56 @@ __global__ __launch_bounds__(64 * NW, 1) void k_attn_split(const AttnArgs) {
         }
 }
 
-// One wave per (query, head): the chunks' outputs joined in their order.
+// One wave per (query, head): the chunks' outputs joined in their order.  Lane
+// s holds the factor of chunk s (64 at a time); loads go 8 chunks at once.
 __global__ __launch_bounds__(256) void k_attn_merge(const AttnArgs) {
     const Args a = arguments();
+    const int lane = lane_id(), splits = a->splits, d = a->d;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + wave_id(), rows = static_cast<int64_t>(a->b) * a->hq * a->sq;
     if (at >= rows) return;
-    const float* ml = a->part + 2 * at * a->splits;
-    const float* o = a->part + 2 * rows * a->splits + at * a->splits * a->d;
+    const float* ml = a->part + 2 * at * splits;
+    const float* o = a->part + 2 * rows * splits + at * splits * d;
     float m = neg_inf(), l = 0.0f;
-    for (int s = 0; s < a->splits; ++s) m = fmaxf(m, ml[2 * s + 1] != 0.0f ? ml[2 * s] : neg_inf());
+    for (int s = lane; s < splits; s += 64) m = fmaxf(m, ml[2 * s + 1] != 0.0f ? ml[2 * s] : neg_inf());
+#pragma unroll
+    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
     const float ms = m == neg_inf() ? 0.0f : m;
-    const int c = 2 * lane_id();
+    const int c = 2 * lane, cc = c < d ? c : 0;
     float x = 0.0f, y = 0.0f;
-    for (int s = 0; s < a->splits; ++s) {
-        const float ls = ml[2 * s + 1];
-        if (ls == 0.0f) continue;  // nothing was seen, nothing written
-        const float f = exp2_fast(ml[2 * s] - ms);
-        l = fmaf(ls, f, l);
-        if (c < a->d) {
-            x = fmaf(o[s * a->d + c], f, x);
-            y = fmaf(o[s * a->d + c + 1], f, y);
+    for (int s0 = 0; s0 < splits; s0 += 64) {
+        const int s = s0 + lane, n = splits - s0 < 64 ? splits - s0 : 64;
+        // a chunk with a sum of zero saw nothing and wrote nothing
+        float ls = s < splits ? ml[2 * s + 1] : 0.0f;
+        const float f = ls != 0.0f ? exp2_fast(ml[2 * s] - ms) : 0.0f;
+        const uint64_t live = __ballot(ls != 0.0f);
+        ls *= f;
+#pragma unroll
+        for (int w = 32; w; w >>= 1) ls += __shfl_xor(ls, w);
+        l += ls;
+        for (int e = 0; e < n; e += 8) {
+            f32x2_t v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int r = e + u < n ? e + u : e;
+                v[u] = *reinterpret_cast<const f32x2_t*>(o + static_cast<int64_t>(s0 + r) * d + cc);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float g = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), (e + u) & 63));
+                if (e + u < n && ((live >> (e + u)) & 1)) {
+                    x = fmaf(v[u].x, g, x);
+                    y = fmaf(v[u].y, g, y);
+                }
+            }
         }
     }
     const bool empty = l == 0.0f;
     const float inv = empty ? 0.0f : 1.0f / l;
     const int i = static_cast<int>(at % a->sq), h = static_cast<int>(at / a->sq % a->hq), b = static_cast<int>(at / a->sq / a->hq);
-    if (c < a->d)
+    if (c < d)
         *reinterpret_cast<uint32_t*>(a->out + b * a->o_b + h * a->o_h + static_cast<int64_t>(i) * a->o_s + c) =
             f32x2_to_bf16x2(x * inv, y * inv);
-    if (lane_id() == 0) a->lse[at] = empty ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (lane == 0) a->lse[at] = empty ? neg_inf() : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 // (lowest, highest) document of each kTile tokens, one wave per tile.
@@ -389,9 +410,11 @@ void fwd(const AttnArgs& a, hipStream_t stream) {
 
 template <int DP, int MOD>
 void split(const AttnArgs& a, hipStream_t stream) {
-    constexpr int NW = 4;
     const int blocks = (a.grp * a.sq + 31) / 32 * a.splits * a.b * a.hkv;
-    k_attn_split<DP, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    // 8 waves fill a CU's LDS with tiles of 64; with more workgroups than CUs
+    // two of 4 waves share it, one computing while the other starts or ends
+    if (DP == 64 && blocks <= 256) k_attn_split<DP, DP == 64 ? 8 : 4, MOD><<<blocks, 64 * (DP == 64 ? 8 : 4), 0, stream>>>(a);
+    else k_attn_split<DP, 4, MOD><<<blocks, 64 * 4, 0, stream>>>(a);
     if (a.splits > 1) {
         const int64_t rows = static_cast<int64_t>(a.b) * a.hq * a.sq;
         k_attn_merge<<<static_cast<int>((rows + 3) / 4), 256, 0, stream>>>(a);

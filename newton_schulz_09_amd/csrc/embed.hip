@@ -120,27 +120,25 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const EmbedArgs 
     __syncthreads();
     const int64_t part = ((a.n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
     const int64_t i0 = wave * part, i1 = i0 + part < a.n ? i0 + part : a.n;
-    constexpr int U = 8;
-    // f(place, token relative to lo, mine) for the part's tokens, 64 at a time
+    constexpr int U = 16;
+    auto token = [&](int64_t at) {  // as 32 bits; all ones: outside the table
+        if (a.tokens64) {
+            const u32x2 w = static_cast<const u32x2*>(a.tokens)[at];
+            return w.y == 0 ? w.x : 0xffffffffu;
+        }
+        return static_cast<const uint32_t*>(a.tokens)[at];
+    };
+    // f(place, token) for the part's tokens, 64 at a time
     auto walk = [&](auto&& f) {
-        for (int64_t i = i0; i < i1; i += 64 * U) {
+        int64_t i = i0;
+        for (; i + 64 * U <= i1; i += 64 * U) {
             uint32_t t[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                t[k] = 0xffffffffu;  // outside the table
-                const int64_t at = i + 64 * k + lane;
-                if (at < i1) {
-                    if (a.tokens64) {
-                        const u32x2 w = static_cast<const u32x2*>(a.tokens)[at];
-                        t[k] = w.y == 0 ? w.x : 0xffffffffu;
-                    } else {
-                        t[k] = static_cast<const uint32_t*>(a.tokens)[at];
-                    }
-                }
-            }
+            for (int k = 0; k < U; ++k) t[k] = token(i + 64 * k + lane);
 #pragma unroll
             for (int k = 0; k < U; ++k) f(i + 64 * k + lane, t[k]);
         }
+        for (; i < i1; i += 64) f(i + lane, i + lane < i1 ? token(i + lane) : 0xffffffffu);
     };
     int32_t low = 0, listed = 0;
     walk([&](int64_t i, uint32_t t) {

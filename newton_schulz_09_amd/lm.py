@@ -53,8 +53,14 @@ _ATTN = struct.Struct("9Q15q2Qq3Q8q2d")
 _QK = struct.Struct("10Q12q2qQqQ3qqd")
 
 
+# the current stream of a device as a number (0.1 us; a Stream object for it costs 2)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _tensor(t, name, dtype, dev, dims=None):
     """Checks one tensor; `dtype` is a type or a tuple of types."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.device == dev and (dims is None or t.dim() == dims):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev or dev.type != "cuda":
@@ -66,7 +72,7 @@ def _tensor(t, name, dtype, dev, dims=None):
 
 
 def _last(t, name):
-    if t.stride(-1) != 1 and t.size(-1) > 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
@@ -91,11 +97,12 @@ def _ws(workspace, need, dev):
 
 def _call(dev, fn, *args):
     """Calls fn(*args, stream) with `dev` as the current device."""
-    if dev.index is not None and dev.index != torch.cuda.current_device():
+    index = dev.index
+    if index is not None and index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(index))
     else:
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+        status = fn(*args, _raw_stream(torch.cuda.current_device() if index is None else index))
     if status:
         muon._check(status)
 
@@ -103,15 +110,15 @@ def _call(dev, fn, *args):
 def _attention_args(q, k, v, out, lse, dout, grads, scale, causal, window, softcap, slopes, documents, prefix, lengths,
                     starts):
     """The checked arguments as muon_attention_args, and the tensors it points to."""
-    dev = q.device if isinstance(q, torch.Tensor) else None
-    if dev is None:
+    if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
+    dev = q.device
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         _tensor(t, name, _BF16, dev, 4)
         _last(t, name)
     b, sq, hq, d = q.shape
-    sk, hkv = k.shape[1], k.shape[2]
-    if k.shape[0] != b or k.shape[3] != d or v.shape != k.shape:
+    kb, sk, hkv, kd = k.shape
+    if kb != b or kd != d or v.shape != k.shape:
         raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit: (batch, positions, "
                          "heads, head size), k and v alike")
     if hkv == 0 or hq % hkv:
@@ -142,7 +149,7 @@ def _attention_args(q, k, v, out, lse, dout, grads, scale, causal, window, softc
         _exactly(starts, "starts", torch.int32, dev, (b,))
         p_starts = starts.data_ptr()
     if out is None:
-        out = torch.empty((b, sq, hq, d), dtype=_BF16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         _tensor(out, "out", _BF16, dev, 4)
         _last(out, "out")
@@ -210,7 +217,7 @@ def attention_backward(dout, q, k, v, out, lse, scale=None, causal=True, window=
     grads = []
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
         if t is None:
-            t = torch.empty(like.shape, dtype=_BF16, device=dev)
+            t = torch.empty_like(like, memory_format=torch.contiguous_format)
         else:
             _exactly(t, name, _BF16, dev, like.shape)
         grads.append(t)
@@ -251,7 +258,7 @@ def _qk_args(q, k, table, positions, q_weight, k_weight, eps, outs, dz, dws):
     results = []
     for t, like, name in ((outs[0], q, outs[2] + "q"), (outs[1], k, outs[2] + "k")):
         if t is None:
-            t = torch.empty(like.shape, dtype=dtype, device=dev)
+            t = torch.empty_like(like, memory_format=torch.contiguous_format)
         else:
             _exactly(t, name, dtype, dev, like.shape)
         results.append(t)
