@@ -52,7 +52,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
     const int i1 = i0 + BM < a->sq ? i0 + BM : a->sq;
     const Seq seq = sequence(a, b);
     const int w0 = i0 + wave_id() * 32, w1 = w0 + 32 < a->sq ? w0 + 32 : a->sq;
-    const Span g = query_span(seq, a, i0, i1), w = query_span(seq, a, w0, w1);
+    Span g = query_span(seq, a, i0, i1), w = query_span(seq, a, w0, w1);
 
     Direct<DP, NT> lk, lv;
     lk.init(a->k + b * a->k_b + kvh * a->k_h, a->k_s, seq.n, a->d);
@@ -61,6 +61,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
     const int sk = a->sk;
     KeyTiles it;
     it.init(seq, a, g, w);
+    in_vectors(g);
+    in_vectors(w);
     int tile[ST], mode[ST];
     auto fetch = [&](int x) {
         tile[x] = it.next(seq, a, g, w, mode[x]);
@@ -119,15 +121,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
         };
         auto grads = [&](int kb, int i) {
             grad1<MOD>(sc, s[kb], dp[kb], i, lse,
-                       fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + 8 * (i / 4) + i % 4)));
+                       fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + place(i))));
         };
         auto finish = [&](int kb) {
             if (masked) {
-                const Hide hide = hide_of(row, seq, a, k0, h4);
-                each<0, 16>([&](auto i_) {
-                    constexpr int i = decltype(i_)::value;
-                    if (!seen(hide, 32 * kb + 8 * (i / 4) + i % 4, sdoc ? sdoc + h4 : nullptr)) dp[kb][i] = 0.0f;
-                });
+                const Bits m = keys_seen(row, seq, a, k0 + h4);
+                each<0, 16>([&](auto i) { dp[kb][i.value] = where(m, kb, i.value, dp[kb][i.value], 0.0f); });
+                if (sdoc)
+                    each<0, 16>([&](auto i_) {
+                        constexpr int i = decltype(i_)::value;
+                        dp[kb][i] = sdoc[32 * kb + place(i) + h4] == row.doc ? dp[kb][i] : 0.0f;
+                    });
             }
             p[kb][0] = pack(dp[kb], 0);
             p[kb][1] = pack(dp[kb], 1);
@@ -187,6 +191,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
     static_assert(ST == 2 || ST == 3, "the waits below count one tile ahead");
     __shared__ __align__(16) bf16_t lds[ST][2][Tile<DP>::ELEMS];
     __shared__ __align__(16) float sstat[ST][2][kTile];
+    __shared__ __align__(16) int sdocs[ST][kTile];
     const Args a = arguments();
     const int U = a->b * a->hkv;
     const int blk = blockIdx.x, u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
@@ -200,7 +205,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
         doc_range(seq, a, r.p0, r.p1, r.d0, r.d1);
         return r;
     };
-    const Span g = key_span(j0, j0 + BN), w = key_span(w0, w0 + 32);
+    Span g = key_span(j0, j0 + BN), w = key_span(w0, w0 + 32);
     // whole blocks of real keys only: the rest is masked one by one
     const bool whole = w0 + 32 <= seq.n;
     const int j = w0 + (lane_id() & 31);
@@ -212,6 +217,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
     // the tiles of all the heads that share the keys, one after the other
     QueryTiles it;
     it.init(seq, a, g, w);
+    in_vectors(g);
+    in_vectors(w);
     Direct<DP, NT> lq, ld;
     lq.init(a->q + b * a->q_b + static_cast<int64_t>(kvh) * a->grp * a->q_h, a->q_s, it.rows, a->d);
     ld.init(a->dout + b * a->do_b + static_cast<int64_t>(kvh) * a->grp * a->do_h, a->do_s, it.rows, a->d);
@@ -239,6 +246,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
         ld.load(row0, at + (2 * x + 1) * TB);
         load_values(stat, row0, it.rows, lds_addr(sstat[x][0]));
         load_values(stat + again(a)->delta_at, row0, it.rows, lds_addr(sstat[x][1]));
+        if (seq.doc) load_docs(seq.doc, seq.start + row0, again(a)->sk, lds_addr(sdocs[x]));
     };
 #pragma unroll
     for (int x = 0; x < ST - 1; ++x) fetch(x);
@@ -253,7 +261,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
     settle(vf);
 
     constexpr int KT = DP / 16, DT = DP / 32;
-    auto step = [&](uint32_t tq, uint32_t td, const float* sl, const float* sdel, bool masked, const Score& score, int q0) {
+    auto step = [&](uint32_t tq, uint32_t td, const float* sl, const float* sdel, const int* sdoc, bool masked, const Score& score, int q0) {
         const int h4 = 4 * (lane_id() >> 5);
         f32x16 s[2], dp[2];
         bf16x8 pp[2][2], pd[2][2], ring[kAhead];
@@ -276,14 +284,19 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
         };
         auto finish = [&](int qb) {
             if (masked) {
-                const Args z = again(a);
-                each<0, 16>([&](auto i_) {
-                    constexpr int i = decltype(i_)::value;
-                    const int p = seq.start + q0 + 32 * qb + 8 * (i / 4) + h4 + i % 4;
-                    bool vis = p >= col.lo && p <= col.hi;
-                    if (seq.doc) vis = vis && doc_of(seq, z, p) == col.doc;
-                    if (!vis) s[qb][i] = dp[qb][i] = 0.0f;
+                const int p0 = seq.start + q0 + h4;
+                const Bits m = bits_of(col.lo - p0, col.hi - p0, 0);
+                each<0, 16>([&](auto i) {
+                    s[qb][i.value] = where(m, qb, i.value, s[qb][i.value], 0.0f);
+                    dp[qb][i.value] = where(m, qb, i.value, dp[qb][i.value], 0.0f);
                 });
+                if (sdoc)
+                    each<0, 16>([&](auto i_) {
+                        constexpr int i = decltype(i_)::value;
+                        const bool mine = sdoc[32 * qb + place(i) + h4] == col.doc;
+                        s[qb][i] = mine ? s[qb][i] : 0.0f;
+                        dp[qb][i] = mine ? dp[qb][i] : 0.0f;
+                    });
             }
             pp[qb][0] = pack(s[qb], 0);
             pp[qb][1] = pack(s[qb], 1);
@@ -325,10 +338,11 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
             constexpr int NL = 2 * Direct<DP, NT>::N + 2;
             if (tile[x] < 0) goto done;
             if (ST == 2 || tile[(x + 1) % ST] < 0) landed<0>();
+            else if (seq.doc) landed<(ST - 2) * (NL + 1)>();
             else landed<(ST - 2) * NL>();
             fetch((x + ST - 1) % ST);
             if (mode[x] != 0)
-                step(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], mode[x] == 1 || !whole, sc[x],
+                step(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x] == 1 || !whole, sc[x],
                      tile[x] * kTile);
         }
     }

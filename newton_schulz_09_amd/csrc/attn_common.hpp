@@ -164,6 +164,13 @@ __device__ __forceinline__ void load_values(const void* p, int row0, int rows, u
     load_lds4(lds, 4 * lane_id(), descriptor(static_cast<const char*>(p) + 4 * static_cast<int64_t>(row0), 4 * left));
 }
 
+// The documents of kTile positions from pos0 on, positions clamped to 0 .. sk - 1.
+__device__ __forceinline__ void load_docs(const int32_t* docs, int pos0, int sk, uint32_t lds) {
+    int p = pos0 + lane_id();
+    p = p < 0 ? 0 : (p < sk ? p : sk - 1);
+    load_lds4(lds, 4 * static_cast<uint32_t>(p), descriptor(docs, 4 * static_cast<uint32_t>(sk)));
+}
+
 // Moves one tile of kTile rows from memory through registers to LDS.  Rows
 // past `rows` and values past the head size come as zeros, whatever memory
 // holds there.
@@ -381,14 +388,28 @@ struct Row {
 __device__ __forceinline__ Row row_of(const Seq& s, Args a, int pos) {
     return {pos, s.doc ? doc_of(s, a, pos) : 0};
 }
-// What hides keys from one query in the tile at k0, relative to the first key
-// of the lane's half: lo <= j <= lo + span (as one unsigned comparison) or j <
-// pre is seen.
-struct Hide {
-    int lo, span, pre, doc;
-    bool none;
+// Which of the 32 results a lane holds of a tile are seen, as bits: result (kb,
+// i) is bit place(i) of word kb, its row 32 kb + place(i) rows past the lane
+// half's first.
+struct Bits {
+    uint32_t w[2];
 };
-__device__ __forceinline__ Hide hide_of(const Row& r, const Seq& s, Args a, int k0, int h4) {
+__device__ constexpr int place(int i) { return 8 * (i / 4) + i % 4; }
+// Rows lo .. hi, and those below pre.
+__device__ __forceinline__ Bits bits_of(int lo, int hi, int pre) {
+    auto below = [](int n) { return n <= 0 ? uint64_t{0} : (n >= 64 ? ~uint64_t{0} : (uint64_t{1} << n) - 1); };
+    const uint64_t m = (below(hi + 1) & ~below(lo)) | below(pre);
+    return {{static_cast<uint32_t>(m), static_cast<uint32_t>(m >> 32)}};
+}
+// x where result (kb, i) is seen, `other` elsewhere: two instructions, and a
+// NaN that is not seen leaves nothing behind.
+__device__ __forceinline__ float where(const Bits& m, int kb, int i, float x, float other) {
+    const uint32_t on = static_cast<uint32_t>(__builtin_amdgcn_sbfe(static_cast<int>(m.w[kb]), place(i), 1));
+    return __uint_as_float((__float_as_uint(x) & on) | (__float_as_uint(other) & ~on));
+}
+// The keys that query r sees of the tile whose first key of the lane's half is
+// j0, but for the document rule.
+__device__ __forceinline__ Bits keys_seen(const Row& r, const Seq& s, Args a, int j0) {
     a = again(a);
     int lo = 0, hi = s.n - 1;
     if (a->causal && r.pos < hi) hi = r.pos;
@@ -396,14 +417,7 @@ __device__ __forceinline__ Hide hide_of(const Row& r, const Seq& s, Args a, int 
         if (r.pos - a->window + 1 > lo) lo = r.pos - a->window + 1;
         if (r.pos + a->window - 1 < hi) hi = r.pos + a->window - 1;
     }
-    return {lo - k0 - h4, hi - lo, s.pre - k0 - h4, r.doc, hi < lo};
-}
-// j: the key relative to k0 + h4; sdoc: the documents of the half's keys, or null.
-__device__ __forceinline__ bool seen(const Hide& h, int j, const int* sdoc) {
-    bool vis = !h.none && static_cast<uint32_t>(j - h.lo) <= static_cast<uint32_t>(h.span);
-    vis = vis || j < h.pre;
-    if (sdoc) vis = vis && sdoc[j] == h.doc;
-    return vis;
+    return bits_of(lo - j0, hi - j0, s.pre - j0);
 }
 
 // Whether a block of queries at positions [p0, p1] (documents in [d0, d1])
@@ -461,11 +475,18 @@ __device__ __forceinline__ Span query_span(const Seq& s, Args a, int i0, int i1)
     return r;
 }
 
+// Keeps what only the tests of tiles use in vector registers: the scalar ones
+// would run out inside the loops.
+__device__ __forceinline__ void in_vectors(Span& r) {
+    asm volatile("" : "+v"(r.p0), "+v"(r.p1), "+v"(r.d0), "+v"(r.d1));
+}
+
 // The key tiles a workgroup's queries see, in order.  64 tiles are tested at
 // a time, one per lane; the answers stay in scalar registers.
 struct KeyTiles {
     uint64_t wg, some, all;
     int base, end;
+    int turns = 1, turn = 0;  // tiles t with t % turns = turn (a power of two)
     __device__ __forceinline__ void fill(const Seq& s, Args a, const Span& g, const Span& w) {
         a = again(a);
         const int t = base + lane_id(), j0 = t * kTile;
@@ -473,14 +494,16 @@ struct KeyTiles {
         if (j1 >= s.n) j1 = s.n - 1;
         int2 e = {0, 0};
         if (s.doc && t < a->n_tiles) e = a->doc_tiles[static_cast<int64_t>(s.b) * a->n_tiles + t];
-        const bool in = t < end;
+        const bool in = t < end && (t & (turns - 1)) == turn;
         const Sight x = sight(s, a, g.p0, g.p1, g.d0, g.d1, j0, j1, e.x, e.y);
         const Sight y = sight(s, a, w.p0, w.p1, w.d0, w.d1, j0, j1, e.x, e.y);
         wg = __ballot(in && x.some);
         some = __ballot(in && w.p0 <= w.p1 && y.some);
         all = __ballot(in && y.all && j0 + kTile <= s.n);
     }
-    __device__ __forceinline__ void init(const Seq& s, Args a, const Span& g, const Span& w) {
+    // of the tiles first .. last - 1
+    __device__ __forceinline__ void init(const Seq& s, Args a, const Span& g, const Span& w, int first = 0,
+                                         int last = 0x7fffffff) {
         int lo = 0, hi = s.n - 1;
         if (a->causal && g.p1 < hi) hi = g.p1;
         if (a->window) {
@@ -492,8 +515,10 @@ struct KeyTiles {
             if (s.pre - 1 > hi) hi = s.pre - 1;
         }
         if (g.p0 > g.p1) hi = -1;
-        base = lo / kTile;
-        end = hi < 0 ? 0 : hi / kTile + 1;
+        base = __builtin_amdgcn_readfirstlane(lo / kTile);
+        end = __builtin_amdgcn_readfirstlane(hi < 0 ? 0 : hi / kTile + 1);
+        base = base > first ? base : first;
+        end = end < last ? end : last;
         wg = some = all = 0;
         if (base < end) fill(s, a, g, w);
     }
@@ -569,8 +594,8 @@ struct QueryTiles {
             }
         }
         if (g.p0 > g.p1) hi = -1;
-        base = lo / kTile;
-        end = hi < 0 ? 0 : hi / kTile + 1;
+        base = __builtin_amdgcn_readfirstlane(lo / kTile);
+        end = __builtin_amdgcn_readfirstlane(hi < 0 ? 0 : hi / kTile + 1);
         wg = some = all = 0;
         if (base < end) fill(s, a, g, w);
     }

@@ -45,7 +45,7 @@ __device__ __forceinline__ void tile_step(Running<DP>& run, const bf16x8 (&qf)[D
     f32x16 s[2];
     auto extras = [&](int kb, int i) {
         float r;
-        const float dist = fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + 8 * (i / 4) + i % 4));
+        const float dist = fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + place(i)));
         s[kb][i] = score<MOD>(sc, s[kb][i], dist, r);
     };
     auto operand = [&](int x) {  // of product x: keys along the row, then V across
@@ -63,11 +63,16 @@ __device__ __forceinline__ void tile_step(Running<DP>& run, const bf16x8 (&qf)[D
     });
     if constexpr (MOD != 0) each<0, 16>([&](auto i) { extras(1, i); });
     if (masked) {
-        const Hide hide = hide_of(row, seq, a, k0, h4);
+        const Bits m = keys_seen(row, seq, a, k0 + h4);
         each<0, 32>([&](auto e) {
             constexpr int kb = decltype(e)::value / 16, i = decltype(e)::value % 16;
-            if (!seen(hide, 32 * kb + 8 * (i / 4) + i % 4, sdoc ? sdoc + h4 : nullptr)) s[kb][i] = neg_inf();
+            s[kb][i] = where(m, kb, i, s[kb][i], neg_inf());
         });
+        if (sdoc)
+            each<0, 32>([&](auto e) {
+                constexpr int kb = decltype(e)::value / 16, i = decltype(e)::value % 16;
+                s[kb][i] = sdoc[32 * kb + place(i) + h4] == row.doc ? s[kb][i] : neg_inf();
+            });
     }
     float top = s[0][0];
     each<1, 32>([&](auto e) { top = fmaxf(top, s[e / 16][e % 16]); });
@@ -116,7 +121,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void k_attn_fwd(const At
     const int i1 = i0 + BM < a->sq ? i0 + BM : a->sq;
     const Seq seq = sequence(a, b);
     const int w0 = i0 + wave_id() * 32, w1 = w0 + 32 < a->sq ? w0 + 32 : a->sq;
-    const Span g = query_span(seq, a, i0, i1), w = query_span(seq, a, w0, w1);
+    Span g = query_span(seq, a, i0, i1), w = query_span(seq, a, w0, w1);
 
     // a ring of ST tiles: ST - 1 are on their way while one is used
     Direct<DP, NT> lk, lv;
@@ -126,6 +131,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void k_attn_fwd(const At
     const int sk = a->sk;
     KeyTiles it;
     it.init(seq, a, g, w);
+    in_vectors(g);
+    in_vectors(w);
     int tile[ST], mode[ST];
     auto fetch = [&](int x) {
         tile[x] = it.next(seq, a, g, w, mode[x]);
@@ -209,7 +216,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_attn_split(const AttnArgs) {
     const int r1 = rt * 32 + 32 < rows ? rt * 32 + 32 : rows;
     // the positions of the tile's rows (whole heads wrap around)
     const bool wraps = rt * 32 / a->sq != (r1 - 1) / a->sq;
-    const Span g = query_span(seq, a, wraps ? 0 : rt * 32 % a->sq, wraps ? a->sq : (r1 - 1) % a->sq + 1);
+    Span g = query_span(seq, a, wraps ? 0 : rt * 32 % a->sq, wraps ? a->sq : (r1 - 1) % a->sq + 1);
 
     bf16x8 qf[DP / 16];
     const Row row = row_of(seq, a, seq.start + i);
@@ -225,18 +232,14 @@ __global__ __launch_bounds__(64 * NW, 1) void k_attn_split(const AttnArgs) {
     Running<DP> run;
     run.init();
 
+    // the chunk's tiles in turn
     KeyTiles it;
-    it.init(seq, a, g, g);
-    const int first = split * a->chunk, last = first + a->chunk;
-    // this wave's next tile of the chunk, in turn over the tiles that are seen
-    int turn = 0;
-    auto next = [&](int& mode) {
-        for (;;) {
-            const int t = it.next(seq, a, g, g, mode);
-            if (t < 0 || t >= last) return -1;
-            if (t >= first && turn++ % NW == wave) return t;
-        }
-    };
+    it.turns = NW;
+    it.turn = wave;
+    it.init(seq, a, g, g, split * a->chunk, split * a->chunk + a->chunk);
+    in_vectors(g);
+    static_assert((NW & (NW - 1)) == 0, "turns");
+    auto next = [&](int& mode) { return it.next(seq, a, g, g, mode); };
     int mode = 0, dcur = 0;
     int t = next(mode);
     auto load = [&](int tile) {
