@@ -11,37 +11,36 @@ namespace {
 
 using namespace attn;
 
-// Result i of a block: s holds q . k (minus lse in the product's units where
-// there are no extras), dp holds dO . v - delta; they become P and dS.
-template <int MOD>
+// Result i of a block: s holds q . k (LSE: minus lse already, in the product's
+// units; else lse2 is subtracted, in units of log 2), dp holds dO . v - delta;
+// they become P and dS.
+template <int MOD, bool LSE>
 __device__ __forceinline__ void grad1(const Score& sc, f32x16& s, f32x16& dp, int i, float lse2, float dist) {
     float r = 0.0f;
-    const float p = exp2_fast(MOD ? score<MOD>(sc, s[i], dist, r) - lse2 : s[i] * sc.c);
+    const float p = exp2_fast(MOD ? score<MOD>(sc, s[i], dist, r) - lse2 : (LSE ? s[i] * sc.c : fmaf(s[i], sc.c, -lse2)));
     float ds = p * dp[i];
     if constexpr (MOD & kCap) ds *= 4.0f * fmaf(-r, r, r);
     s[i] = p;
     dp[i] = ds;
 }
 
-// What the kernels subtract from a row's scores: with extras lse in units of
-// log 2, +inf for a row that saw nothing (its P is then zero); without, -lse
-// in units of the product q . k, where the sums of the products start.
+// What the second kernel subtracts from a row's scores: with extras lse in
+// units of log 2, +inf for a row that saw nothing (its P is then zero);
+// without, -lse in units of the product q . k, where its products start.
 template <int MOD>
 __device__ __forceinline__ float lse_term(float lse, float scale) {
     if constexpr (MOD != 0) return lse == neg_inf() ? __builtin_inff() : lse * kLog2e;
     else return lse == neg_inf() ? neg_inf() : -lse / scale;
 }
 
-constexpr int kAhead = 3;
-
 // dQ.  32 keys are one block; the gradients of the scores of a block are made
 // in the shadow of products of the other block of the tile:
 //     products   S, dP (0)   S, dP (1)   dQ (0)    dQ (1)
 //     vector                 block 0     block 1
-template <int DP, int NW, int ST, int MOD>
+template <int DP, int NW, int MOD>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
     constexpr int BM = 32 * NW, NT = 64 * NW, TB = 2 * Tile<DP>::ELEMS;
-    static_assert(ST == 2 || ST == 3, "the waits below count one tile ahead");
+    constexpr int ST = 2;  // one tile lands while the other is used (with three: 1 to 8 % slower)
     __shared__ __align__(16) bf16_t lds[ST][2][Tile<DP>::ELEMS];
     __shared__ __align__(16) int sdocs[ST][kTile];
     const Args a = arguments();
@@ -71,8 +70,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
         lv.load(tile[x] * kTile, at + (2 * x + 1) * TB);
         if (seq.doc) load_values(seq.doc, tile[x] * kTile, sk, lds_addr(sdocs[x]));
     };
-#pragma unroll
-    for (int x = 0; x < ST - 1; ++x) fetch(x);
+    fetch(0);
 
     const int i = w0 + (lane_id() & 31);
     const Row row = row_of(seq, a, seq.start + i);
@@ -92,10 +90,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
         delta = half_sum(delta);
     }
     const int64_t stat = (static_cast<int64_t>(b) * a->hq + h) * a->sq + i;
-    const float lse = lse_term<MOD>(real ? a->lse[stat] : neg_inf(), a->scale);
+    const float given = real ? a->lse[stat] : neg_inf();
+    const float lse2 = given == neg_inf() ? __builtin_inff() : given * kLog2e;
     if (i < a->sq && lane_id() < 32) {
         // for the second kernel: what it starts its products from
-        a->stats[stat] = lse;
+        a->stats[stat] = lse_term<MOD>(given, a->scale);
         a->stats[stat + a->delta_at] = -delta;
     }
     RowFrag<DP> rf;
@@ -108,19 +107,19 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
     settle(qf);
     settle(dof);
 
-    constexpr int KT = DP / 16, DT = DP / 32;
+    constexpr int KT = DP / 16, DT = DP / 32, kAhead = 3;
     auto step = [&](uint32_t tk, uint32_t tv, bool masked, const int* sdoc, int k0) {
         const int h4 = 4 * (lane_id() >> 5);
         f32x16 s[2], dp[2];
         bf16x8 p[2][2], ring[kAhead];
-        float s0 = MOD ? 0.0f : lse, dp0 = -delta;
-        asm volatile("" : "+v"(s0), "+v"(dp0));  // (their 16 copies are not kept between tiles)
+        float dp0 = -delta;
+        if constexpr (DP > 64) asm volatile("" : "+v"(dp0));  // (no room to keep its 16 copies between tiles)
         auto operand = [&](int y) {  // K and V along the row in turn, both blocks; then K across
             return y < 4 * KT ? rf.read(y % 2 ? tv : tk, y / (2 * KT), y % (2 * KT) / 2)
                               : cf.read(tk, (y - 4 * KT) / DT, (y - 4 * KT) % DT);
         };
         auto grads = [&](int kb, int i) {
-            grad1<MOD>(sc, s[kb], dp[kb], i, lse,
+            grad1<MOD, false>(sc, s[kb], dp[kb], i, lse2,
                        fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + place(i))));
         };
         auto finish = [&](int kb) {
@@ -142,7 +141,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
             constexpr int y = decltype(y_)::value;
             if constexpr (y < 4 * KT) {
                 constexpr int kb = y / (2 * KT), t = y % (2 * KT) / 2;
-                if constexpr (y % 2 == 0) s[kb] = mfma(ring[y % kAhead], qf[t], t == 0 ? splat(s0) : s[kb]);
+                if constexpr (y % 2 == 0) s[kb] = mfma(ring[y % kAhead], qf[t], t == 0 ? splat(0.0f) : s[kb]);
                 else dp[kb] = mfma(ring[y % kAhead], dof[t], t == 0 ? splat(dp0) : dp[kb]);
             } else {
                 constexpr int x = y - 4 * KT, dt = x % DT, kb = x / (2 * DT), t = x / DT % 2;
@@ -162,15 +161,13 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
             in_order();
         });
     };
+    // (the two buffers' code side by side: as one loop, 3 to 25 % slower)
     for (;;) {
 #pragma unroll
         for (int x = 0; x < ST; ++x) {
-            constexpr int NL = 2 * Direct<DP, NT>::N;
             if (tile[x] < 0) goto done;
-            if (ST == 2 || tile[(x + 1) % ST] < 0) landed<0>();
-            else if (seq.doc) landed<(ST - 2) * (NL + 1)>();
-            else landed<(ST - 2) * NL>();
-            fetch((x + ST - 1) % ST);
+            landed();
+            fetch(1 - x);
             if (mode[x] != 0)
                 step(at + 2 * x * TB, at + (2 * x + 1) * TB, mode[x] == 1, seq.doc ? sdocs[x] : nullptr, tile[x] * kTile);
         }
@@ -185,10 +182,10 @@ done:
 // them.  32 queries are one block of a tile; as above
 //     products   S, dP (0)   S, dP (1)   dV, dK (0)   dV, dK (1)
 //     vector                 block 0     block 1
-template <int DP, int NW, int ST, int MOD>
+template <int DP, int NW, int MOD>
 __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const AttnArgs) {
     constexpr int BN = 32 * NW, NT = 64 * NW, TB = 2 * Tile<DP>::ELEMS;
-    static_assert(ST == 2 || ST == 3, "the waits below count one tile ahead");
+    constexpr int ST = 2;  // one tile lands while the other is used (with three: 1 to 8 % slower)
     __shared__ __align__(16) bf16_t lds[ST][2][Tile<DP>::ELEMS];
     __shared__ __align__(16) float sstat[ST][2][kTile];
     __shared__ __align__(16) int sdocs[ST][kTile];
@@ -224,9 +221,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
     ld.init(a->dout + b * a->do_b + static_cast<int64_t>(kvh) * a->grp * a->do_h, a->do_s, it.rows, a->d);
     const float* stat = a->stats + (static_cast<int64_t>(b) * a->hq + kvh * a->grp) * a->sq;
     const uint32_t at = lds_addr(lds);
-    int tile[ST], mode[ST], left = a->grp - 1;
-    Score sc[ST];
-    Score now = score_of<MOD>(a, kvh * a->grp);
+    int tile[ST], mode[ST], left = a->grp - 1;  // heads after the tiles' own
+    Score sc[ST], head = score_of<MOD>(a, kvh * a->grp);
     auto fetch = [&](int x) {
         tile[x] = it.next(seq, a, g, w, mode[x]);
         if (tile[x] < 0 && left > 0) {
@@ -236,10 +232,10 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
             lq.base += z->q_h;
             ld.base += z->do_h;
             stat += z->sq;
-            now = score_of<MOD>(z, kvh * z->grp + z->grp - 1 - left);
+            head = score_of<MOD>(z, kvh * z->grp + z->grp - 1 - left);
             tile[x] = it.next(seq, z, g, w, mode[x]);
         }
-        sc[x] = now;
+        sc[x] = head;
         if (tile[x] < 0) return;
         const int row0 = tile[x] * kTile;
         lq.load(row0, at + 2 * x * TB);
@@ -248,8 +244,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
         load_values(stat + again(a)->delta_at, row0, it.rows, lds_addr(sstat[x][1]));
         if (seq.doc) load_docs(seq.doc, seq.start + row0, again(a)->sk, lds_addr(sdocs[x]));
     };
-#pragma unroll
-    for (int x = 0; x < ST - 1; ++x) fetch(x);
+    fetch(0);
     RowFrag<DP> rf;
     ColFrag<DP> cf;
     rf.init();
@@ -260,7 +255,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
     settle(kf);
     settle(vf);
 
-    constexpr int KT = DP / 16, DT = DP / 32;
+    constexpr int KT = DP / 16, DT = DP / 32, kAhead = DP == 64 ? 3 : 8;
     auto step = [&](uint32_t tq, uint32_t td, const float* sl, const float* sdel, const int* sdoc, bool masked, const Score& score, int q0) {
         const int h4 = 4 * (lane_id() >> 5);
         f32x16 s[2], dp[2];
@@ -279,7 +274,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
         };
         auto grads = [&](int qb, int i) {
             const int r = 32 * qb + 8 * (i / 4) + i % 4;
-            grad1<MOD>(score, s[qb], dp[qb], i, MOD ? sl[r + h4] : 0.0f,
+            grad1<MOD, true>(score, s[qb], dp[qb], i, MOD ? sl[r + h4] : 0.0f,
                        fabsf(static_cast<float>(seq.start + q0 + h4 - col.pos) + static_cast<float>(r)));
         };
         auto finish = [&](int qb) {
@@ -332,15 +327,13 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
             in_order();
         });
     };
+    // (the two buffers' code side by side: as one loop, 3 to 25 % slower)
     for (;;) {
 #pragma unroll
         for (int x = 0; x < ST; ++x) {
-            constexpr int NL = 2 * Direct<DP, NT>::N + 2;
             if (tile[x] < 0) goto done;
-            if (ST == 2 || tile[(x + 1) % ST] < 0) landed<0>();
-            else if (seq.doc) landed<(ST - 2) * (NL + 1)>();
-            else landed<(ST - 2) * NL>();
-            fetch((x + ST - 1) % ST);
+            landed();
+            fetch(1 - x);
             if (mode[x] != 0)
                 step(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x] == 1 || !whole, sc[x],
                      tile[x] * kTile);
@@ -356,15 +349,15 @@ done:
 
 template <int DP, int MOD>
 void dq(const AttnArgs& a, hipStream_t stream) {
-    constexpr int NW = 4, ST = DP == 128 ? 2 : 3, BM = 32 * NW;
+    constexpr int NW = 4, BM = 32 * NW;
     const int blocks = (a.sq + BM - 1) / BM * a.b * a.hq;
-    k_attn_dq<DP, NW, ST, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    k_attn_dq<DP, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
 }
 template <int DP, int MOD>
 void dkv(const AttnArgs& a, hipStream_t stream) {
-    constexpr int NW = 4, ST = 3, BN = 32 * NW;
+    constexpr int NW = 4, BN = 32 * NW;
     const int blocks = (a.sk + BN - 1) / BN * a.b * a.hkv;
-    k_attn_dkv<DP, NW, ST, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    k_attn_dkv<DP, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
 }
 
 }  // namespace

@@ -103,12 +103,9 @@ __device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, u32x4 des
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
                  : "memory");
 }
-// All but this wave's last N loads have landed and its LDS reads are done,
-// and so for every wave of the workgroup.
-template <int N>
-__device__ __forceinline__ void landed() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
-}
+// This wave's loads have landed and its LDS reads are done, and so for every
+// wave of the workgroup.
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 __device__ __forceinline__ u32x4 descriptor(const void* p, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(p);
     return u32x4{static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(a))),
@@ -158,7 +155,7 @@ struct Direct {
     }
 };
 // One 4-byte value of each of kTile rows (row0 < rows), every wave loading all
-// of them (the waves' counts of loads stay equal).
+// of them.
 __device__ __forceinline__ void load_values(const void* p, int row0, int rows, uint32_t lds) {
     const int left = rows - row0 < kTile ? rows - row0 : kTile;
     load_lds4(lds, 4 * lane_id(), descriptor(static_cast<const char*>(p) + 4 * static_cast<int64_t>(row0), 4 * left));
@@ -203,9 +200,10 @@ struct Loader {
         const int left = rows - row0 < kTile ? rows - row0 : kTile;
         const uint32_t bytes = left > 0 ? static_cast<uint32_t>(left - 1) * static_cast<uint32_t>(2 * stride) + row_bytes : 0;
         const auto r = rsrc(base + static_cast<int64_t>(row0) * stride, bytes);
+        // non-temporal: the cache is read once (32 caches of 16384 keys: 312 -> 293 us)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            reg[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff[i], 0, 0));
+            reg[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, voff[i], 0, 2));
     }
     __device__ __forceinline__ void store(bf16_t* tile) {
 #pragma unroll

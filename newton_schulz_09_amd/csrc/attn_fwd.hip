@@ -106,10 +106,10 @@ __device__ __forceinline__ void tile_step(Running<DP>& run, const bf16x8 (&qf)[D
 }
 
 // Workgroups of NW waves, 32 queries of one head each.
-template <int DP, int NW, int ST, int MOD>
+template <int DP, int NW, int MOD>
 __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void k_attn_fwd(const AttnArgs) {
     constexpr int BM = 32 * NW, NT = 64 * NW, TB = 2 * Tile<DP>::ELEMS;
-    static_assert(ST == 2 || ST == 3, "the waits below count one tile ahead");
+    constexpr int ST = 2;  // one tile lands while the other is used (with three: 1 to 8 % slower)
     __shared__ __align__(16) bf16_t lds[ST][2][Tile<DP>::ELEMS];
     __shared__ __align__(16) int sdocs[ST][kTile];
     const Args a = arguments();
@@ -123,7 +123,6 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void k_attn_fwd(const At
     const int w0 = i0 + wave_id() * 32, w1 = w0 + 32 < a->sq ? w0 + 32 : a->sq;
     Span g = query_span(seq, a, i0, i1), w = query_span(seq, a, w0, w1);
 
-    // a ring of ST tiles: ST - 1 are on their way while one is used
     Direct<DP, NT> lk, lv;
     lk.init(a->k + b * a->k_b + kvh * a->k_h, a->k_s, seq.n, a->d);
     lv.init(a->v + b * a->v_b + kvh * a->v_h, a->v_s, seq.n, a->d);
@@ -141,8 +140,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void k_attn_fwd(const At
         lv.load(tile[x] * kTile, at + (2 * x + 1) * TB);
         if (seq.doc) load_values(seq.doc, tile[x] * kTile, sk, lds_addr(sdocs[x]));
     };
-#pragma unroll
-    for (int x = 0; x < ST - 1; ++x) fetch(x);
+    fetch(0);
     const int i = w0 + (lane_id() & 31);
     const Row row = row_of(seq, a, seq.start + i);
     const Score sc = score_of<MOD>(a, h);
@@ -155,22 +153,21 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void k_attn_fwd(const At
     Running<DP> run;
     run.init();
     settle(qf);
+    // (the two buffers' code side by side: as one loop, 3 to 25 % slower)
+    auto use = [&](auto x_) {
+        constexpr int x = decltype(x_)::value;
+        landed();
+        fetch(1 - x);
+        if (mode[x] != 0)
+            tile_step<DP, MOD>(run, qf, rf, cf, at + 2 * x * TB, at + (2 * x + 1) * TB, mode[x] == 1,
+                               seq.doc ? sdocs[x] : nullptr, row, sc, seq, a, tile[x] * kTile);
+    };
     for (;;) {
-#pragma unroll
-        for (int x = 0; x < ST; ++x) {
-            constexpr int NL = 2 * Direct<DP, NT>::N;
-            if (tile[x] < 0) goto done;
-            // the loads of the tile after this one may still be on their way
-            if (ST == 2 || tile[(x + 1) % ST] < 0) landed<0>();
-            else if (seq.doc) landed<(ST - 2) * (NL + 1)>();
-            else landed<(ST - 2) * NL>();
-            fetch((x + ST - 1) % ST);
-            if (mode[x] != 0)
-                tile_step<DP, MOD>(run, qf, rf, cf, at + 2 * x * TB, at + (2 * x + 1) * TB, mode[x] == 1,
-                                   seq.doc ? sdocs[x] : nullptr, row, sc, seq, a, tile[x] * kTile);
-        }
+        if (tile[0] < 0) break;
+        use(std::integral_constant<int, 0>{});
+        if (tile[1] < 0) break;
+        use(std::integral_constant<int, 1>{});
     }
-done:
     const Args z = again(a);
     const bool ok = i < z->sq;
     const float l = half_sum(run.l);
@@ -406,9 +403,9 @@ __global__ __launch_bounds__(256) void k_doc_tiles(const AttnArgs) {
 
 template <int DP, int MOD>
 void fwd(const AttnArgs& a, hipStream_t stream) {
-    constexpr int NW = 4, ST = DP == 128 ? 2 : 3, BM = 32 * NW;
+    constexpr int NW = 4, BM = 32 * NW;
     const int blocks = (a.sq + BM - 1) / BM * a.b * a.hq;
-    k_attn_fwd<DP, NW, ST, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    k_attn_fwd<DP, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
 }
 
 template <int DP, int MOD>

@@ -86,12 +86,15 @@ struct AttnPlan {
     size_t off_docs, off_part, off_stats, bytes;
 };
 
-// Few rows per key head (a step of generation), or too few workgroups of
-// whole row blocks to fill the chip: the keys are split.
+// Few rows per key head (a step of generation), or many keys and at most 48
+// blocks of 128 queries for 256 CUs: the keys are split.  (64 queries of 32
+// heads of 128 over 16384 keys, 32 blocks: 301 -> 86 us; 256 of 24 heads over
+// 2048, 48 blocks: 42 -> 39; 2048 of 6 heads, 96 blocks: 43 -> 57, not split.)
 AttnPlan plan_forward(const muon_attention_args* x) {
     AttnPlan p{};
     const int64_t grp = x->heads / x->kv_heads, rows = grp * x->sq, tiles = div_up(x->sk, kTile);
-    p.split = rows <= 32;
+    const int64_t blocks = div_up(x->sq, 128) * x->batch * x->heads;
+    p.split = rows <= 32 || (blocks <= 48 && tiles >= 32);
     p.splits = 1;
     p.chunk = static_cast<int>(tiles > 0 ? tiles : 1);
     if (p.split) {
