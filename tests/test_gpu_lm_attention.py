@@ -230,3 +230,30 @@ def test_gradient_against_differences(lm):
     pred = sum((t.cpu().double() * x).sum().item() for t, x in zip(grads, dirs))
     room = sum((tol[n] * x.abs()).sum().item() for n, x in zip(("dq", "dk", "dv"), dirs))
     assert math.isfinite(pred) and abs(pred - slope) <= room + 1e-4 * abs(slope)
+
+
+@pytest.mark.parametrize("sq,sk,hq,hkv,d", [(130, 2100, 4, 1, 64), (40, 4400, 8, 2, 128), (513, 2049, 2, 2, 96)])
+@pytest.mark.parametrize("name", ["none", "all", "prefix", "documents not causal", "length 0 and 1"])
+def test_few_blocks_over_many_keys(lm, sq, sk, hq, hkv, d, name):
+    kw = dict(MASKS[name]) if name != "none" else {}
+    if "lengths" in kw and name == "all":
+        kw["lengths"] = (sk - 100, sk // 2)
+        kw["starts"] = (sk - 100 - sq, sk // 2 - sq + 3)
+        kw["window"], kw["documents"] = 1500, 900
+    check(lm, *make(2, sq, sk, hq, hkv, d), backward=False, **masks(kw, 2, sq, sk, hq))
+
+
+def test_documents_at_clamped_positions(lm):
+    """Positions before the first and after the last key take the document there."""
+    q, k, v, dout = make(2, 200, 150, 2, 1, 64)
+    check(lm, q, k, v, dout, documents=docs(2, 150, 30), starts=ints(-40, 30), causal=False)
+    check(lm, q, k, v, dout, documents=docs(2, 150, 30), starts=ints(-40, 30), window=60)
+
+
+def test_nan_at_keys_that_are_masked_but_never_read(lm):
+    """A NaN key hidden by the causal mask does not reach the queries before it."""
+    q, k, v, dout = make(1, 100, 100, 2, 2, 64)
+    clean = lm.attention(q, k, v)[0][:, :90].clone()
+    k[:, 90:] = float("nan")
+    got = lm.attention(q, k, v)[0]
+    assert torch.equal(got[:, :90], clean) and torch.isnan(got[:, 90:]).all()
