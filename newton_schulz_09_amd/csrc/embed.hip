@@ -6,7 +6,7 @@
 // stable), then sums windows of sorted entries and writes the rows of tokens
 // that do not occur (k_embed_sum), so that a token's work is spread over many
 // workgroups however often it occurs, and last joins the runs that cross
-// windows (k_embed_join).
+// windows (k_embed_join).  Few tokens take one launch (k_embed_direct).
 #include "../../include/muon.h"
 #include "lm_common.hpp"
 
@@ -336,6 +336,79 @@ __global__ __launch_bounds__(256) void k_embed_join(const EmbedArgs a) {
     store_e<TD, V>(static_cast<TD*>(a.dst) + static_cast<int64_t>(t) * a.width + c, acc);
 }
 
+// Few tokens, in one launch: a workgroup owns `rows` rows of the table.  Its 4
+// waves look through a quarter of the tokens each and list the workgroup's own
+// in order; one wave sorts them by row, stably; then groups of `lanes` threads
+// take a row each.  Bound by the table's zeros (999 tokens, 50257 x 1600
+// bfloat16: 161 MB).
+constexpr int kDirectTokens = 1024;
+constexpr int kDirectRows = 32;
+template <typename TS, typename TD, int V>
+__global__ __launch_bounds__(256) void k_embed_direct(const EmbedArgs a, int rows, int lanes) {
+    __shared__ uint32_t list[4][kDirectTokens / 4];  // token's place * kDirectRows + row
+    __shared__ uint16_t sorted[kDirectTokens];
+    __shared__ int32_t count[4], first[kDirectRows + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows;
+    const int mine = a.vocab - r0 < rows ? static_cast<int>(a.vocab - r0) : rows;
+    const int n = static_cast<int>(a.n), part = (n + 3) / 4;
+    const int i1 = (wave + 1) * part < n ? (wave + 1) * part : n;
+    int listed = 0;
+    for (int i = wave * part; i < i1; i += 64) {
+        const int64_t y = i + lane < i1 ? token_at(a, i + lane) - r0 : -1;
+        const bool in = y >= 0 && y < mine;
+        const uint64_t all = __ballot(in);
+        if (in) list[wave][listed + __popcll(all & ((1ull << lane) - 1))] = (i + lane) * kDirectRows + static_cast<int>(y);
+        listed += __popcll(all);
+    }
+    if (lane == 0) count[wave] = listed;
+    __syncthreads();
+    if (wave == 0) {
+        // lane r < kDirectRows: row r
+        int c = 0;
+        for (int w = 0; w < 4; ++w)
+            for (int e = 0; e < count[w]; ++e) c += static_cast<int>(list[w][e] % kDirectRows) == lane;
+        int incl = c;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const int y = __shfl_up(incl, m);
+            if (lane >= m) incl += y;
+        }
+        int at = incl - c;
+        if (lane <= kDirectRows) first[lane] = at;
+        for (int w = 0; w < 4; ++w)
+            for (int e = 0; e < count[w]; ++e) {
+                const uint32_t u = list[w][e];
+                if (static_cast<int>(u % kDirectRows) == lane) sorted[at++] = static_cast<uint16_t>(u / kDirectRows);
+            }
+    }
+    __syncthreads();
+    const int c = (static_cast<int>(blockIdx.y) * lanes + static_cast<int>(threadIdx.x) % lanes) * V;
+    if (c >= a.width) return;
+    const TS* src = static_cast<const TS*>(a.src) + c;
+    for (int r = threadIdx.x / lanes; r < mine; r += 256 / lanes) {
+        const int e0 = first[r], e1 = first[r + 1];
+        float acc[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] = 0.0f;
+        constexpr int U = 8;
+        for (int e = e0; e < e1; e += U) {
+            float x[U][V];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                load_e<TS, V>(src + static_cast<int64_t>(sorted[e + u < e1 ? e + u : e]) * a.width, x[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (e + u < e1)
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc[k] += x[u][k];
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) acc[k] *= a.scale;
+        store_e<TD, V>(static_cast<TD*>(a.dst) + (r0 + r) * a.width + c, acc);
+    }
+}
+
 int row_lanes(int pieces) {
     int lanes = 1;
     while (lanes < 64 && lanes < pieces) lanes <<= 1;
@@ -350,13 +423,24 @@ void fwd(const EmbedArgs& a, hipStream_t stream) {
 
 template <typename TS, typename TD, int V>
 void bwd(const EmbedArgs& a, hipStream_t stream) {
+    // pieces whose stores are contiguous over a wave
+    constexpr int W = V == 1 ? 1 : (sizeof(TS) == 2 && sizeof(TD) == 2 ? 8 : 4), J = V == 1 ? 1 : 4;
+    const int pieces = a.width / W;
+    if (a.n <= kDirectTokens) {
+        // a workgroup per CU at least, where the table has the rows
+        int64_t rows = a.vocab / 256;
+        rows = rows < 1 ? 1 : (rows < kDirectRows ? rows : kDirectRows);
+        int lanes = 1;
+        while (lanes < 256 && lanes < pieces) lanes <<= 1;
+        k_embed_direct<TS, TD, W><<<dim3(static_cast<uint32_t>((a.vocab + rows - 1) / rows),
+                                         static_cast<uint32_t>((pieces + lanes - 1) / lanes)),
+                                    256, 0, stream>>>(a, static_cast<int>(rows), lanes);
+        return;
+    }
     // 256 workgroups, one per CU, unless the table needs more
     int64_t span = (a.vocab + 255) / 256;
     if (span > kSortSpan) span = kSortSpan;
     k_embed_sort<<<static_cast<uint32_t>((a.vocab + span - 1) / span), 64 * kSortWaves, 0, stream>>>(a, static_cast<int>(span));
-    // pieces whose stores are contiguous over a wave
-    constexpr int W = V == 1 ? 1 : (sizeof(TS) == 2 && sizeof(TD) == 2 ? 8 : 4), J = V == 1 ? 1 : 4;
-    const int pieces = a.width / W;
     int threads = (pieces + 63) / 64 * 64;
     if (threads > 256) threads = 256;
     const int64_t windows = (a.n + a.window - 1) / a.window, zeros = (a.vocab + kZeroRows - 1) / kZeroRows;

@@ -303,8 +303,8 @@ bool embed_sizes_ok(int64_t n, int64_t vocab, int64_t width) {
     return n >= 0 && vocab > 0 && width > 0 && n < kMaxBlocks && vocab < kMaxBlocks && width <= (1 << 20) &&
            times(n, width) >= 0 && times(vocab, width) >= 0;
 }
-// 8 entries for a few tokens (one batch of loads), 32 for many: longer windows
-// leave fewer sums to join, shorter ones keep more of the chip busy.
+// 8 entries for a few thousand tokens (one batch of loads), 32 for many: longer
+// windows leave fewer sums to join, shorter ones keep more of the chip busy.
 int embed_window(int64_t n) {
     int w = 8;
     while (w < 32 && n / (2 * w) >= 512) w *= 2;

@@ -208,3 +208,12 @@ def test_graph(lm):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want)), seed
+
+
+@pytest.mark.parametrize("n", [1023, 1024, 1025, 2000])
+@pytest.mark.parametrize("vocab,width", [(1, 64), (33, 8), (300, 2064), (8200, 96), (700, 7)])
+def test_embedding_gradient_at_the_borders_of_its_variants(lm, n, vocab, width):
+    g = torch.Generator().manual_seed(n + vocab)
+    tokens = (torch.rand(n, generator=g, dtype=torch.float64) ** 3 * vocab).long()
+    check_embed(lm, tokens.cuda(), vocab, width, torch.bfloat16, torch.bfloat16, 1.0)
+    check_embed(lm, tokens.int().cuda(), vocab, width, torch.float32, torch.bfloat16, 0.5)
