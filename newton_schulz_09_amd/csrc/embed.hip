@@ -107,6 +107,7 @@ __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a, int lanes) {
 constexpr int kSortWaves = 16;
 constexpr int kSortSpan = 512;   // table rows per workgroup at most
 constexpr int kSortList = 1024;  // entries a wave can list
+template <bool T64>
 __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const EmbedArgs a, int span) {
     __shared__ int32_t cnt[kSortWaves][kSortSpan];
     __shared__ uint32_t list[kSortWaves][kSortList];  // place in the part * kSortSpan + row
@@ -121,24 +122,26 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const EmbedArgs 
     const int64_t part = ((a.n + kSortWaves - 1) / kSortWaves + 63) / 64 * 64;
     const int64_t i0 = wave * part, i1 = i0 + part < a.n ? i0 + part : a.n;
     constexpr int U = 16;
-    auto token = [&](int64_t at) {  // as 32 bits; all ones: outside the table
-        if (a.tokens64) {
-            const u32x2 w = static_cast<const u32x2*>(a.tokens)[at];
-            return w.y == 0 ? w.x : 0xffffffffu;
-        }
-        return static_cast<const uint32_t*>(a.tokens)[at];
+    // tokens as 32 bits (all ones: outside the table), all of a batch in flight
+    auto load = [&](int64_t at) {
+        if constexpr (T64) return static_cast<const u32x2*>(a.tokens)[at];
+        else return static_cast<const uint32_t*>(a.tokens)[at];
+    };
+    auto narrow = [](auto w) -> uint32_t {
+        if constexpr (T64) return w.y == 0 ? w.x : 0xffffffffu;
+        else return w;
     };
     // f(place, token) for the part's tokens, 64 at a time
     auto walk = [&](auto&& f) {
         int64_t i = i0;
         for (; i + 64 * U <= i1; i += 64 * U) {
-            uint32_t t[U];
+            decltype(load(0)) t[U];
 #pragma unroll
-            for (int k = 0; k < U; ++k) t[k] = token(i + 64 * k + lane);
+            for (int k = 0; k < U; ++k) t[k] = load(i + 64 * k + lane);
 #pragma unroll
-            for (int k = 0; k < U; ++k) f(i + 64 * k + lane, t[k]);
+            for (int k = 0; k < U; ++k) f(i + 64 * k + lane, narrow(t[k]));
         }
-        for (; i < i1; i += 64) f(i + lane, i + lane < i1 ? token(i + lane) : 0xffffffffu);
+        for (; i < i1; i += 64) f(i + lane, i + lane < i1 ? narrow(load(i + lane)) : 0xffffffffu);
     };
     int32_t low = 0, listed = 0;
     walk([&](int64_t i, uint32_t t) {
@@ -440,7 +443,9 @@ void bwd(const EmbedArgs& a, hipStream_t stream) {
     // 256 workgroups, one per CU, unless the table needs more
     int64_t span = (a.vocab + 255) / 256;
     if (span > kSortSpan) span = kSortSpan;
-    k_embed_sort<<<static_cast<uint32_t>((a.vocab + span - 1) / span), 64 * kSortWaves, 0, stream>>>(a, static_cast<int>(span));
+    const uint32_t sorts = static_cast<uint32_t>((a.vocab + span - 1) / span);
+    if (a.tokens64) k_embed_sort<true><<<sorts, 64 * kSortWaves, 0, stream>>>(a, static_cast<int>(span));
+    else k_embed_sort<false><<<sorts, 64 * kSortWaves, 0, stream>>>(a, static_cast<int>(span));
     int threads = (pieces + 63) / 64 * 64;
     if (threads > 256) threads = 256;
     const int64_t windows = (a.n + a.window - 1) / a.window, zeros = (a.vocab + kZeroRows - 1) / kZeroRows;
