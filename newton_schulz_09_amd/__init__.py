@@ -4,6 +4,8 @@ the C-ABI library ``libmuon.so`` (declared in ``include/muon.h``).
 
 ``newton_schulz_09_amd.muon`` is the Python binding (argument marshalling
 only; it raises if the HIP library is missing).  ``workloads`` holds the
-seeded synthetic inputs.
+seeded synthetic inputs.  ``lm`` binds the operators of the model around the
+step (``include/muon_lm.h``): attention, the norm and rotation of heads, and
+the embedding, with their gradients; ``lm_example`` uses them together.
 """
-__all__ = ["muon", "workloads"]
+__all__ = ["lm", "muon", "workloads"]
