@@ -55,7 +55,8 @@ extern "C" {
  * of the batch through 0 * inf.)
  *
  * Scores, statistics and sums are float32.  exp(z - lse) and the gradient of
- * the scores are rounded to bfloat16 as operands of the matrix cores.
+ * the scores are rounded to bfloat16 as operands of the matrix cores; the
+ * backward pass takes sum dout out from the rounded out it is given.
  */
 typedef struct muon_attention_args {
     const uint16_t *q;      /* [batch][sq][heads][d], bfloat16 */

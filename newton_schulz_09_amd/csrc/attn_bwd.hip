@@ -3,6 +3,12 @@
 // walked per block of queries, then dK and dV with the queries walked per
 // block of keys.  P is made again from the scores and lse; recomputing the
 // two products S and dO V^T costs 7 products instead of 5.
+//
+// 16 x 1024 tokens of 12 heads of 64, causal: dQ 61 us, dK and dV 72, both bound
+// by vector work (an exponential and 4 other instructions a score) and its
+// waits.  One packed sequence of 16384 tokens, 6 heads of 128, capped scores,
+// window 4096, documents: 195 and 257 us.  delta = sum dO O is taken from the
+// bf16 O that the caller holds.
 #include "attn_common.hpp"
 
 namespace muon {

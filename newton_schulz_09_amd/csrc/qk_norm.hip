@@ -7,8 +7,10 @@
 //
 // Bound by memory: every head is read once and written once.  A head is held
 // by 2^k lanes, each with one 16-byte piece of either half, so the rotation
-// needs no exchange between lanes and the norm k of them; a wave takes one
-// token at a time, whose angles its lanes load once for all heads.
+// needs no exchange between lanes and the norm k of them.  Such a group takes
+// the heads of one token in turn (65536 tokens of 12 + 12 bf16 heads of 64: 93 us
+// and 139 with gradients, 90 % of the rate of a large copy; a wave per token,
+// its groups side by side on the heads: 163 and 265).
 #include <type_traits>
 
 #include "../../include/muon.h"
