@@ -7,7 +7,7 @@
 // 16 x 1024 tokens of 12 heads of 64, causal: dQ 61 us, dK and dV 72, both bound
 // by vector work (an exponential and 4 other instructions a score) and its
 // waits.  One packed sequence of 16384 tokens, 6 heads of 128, capped scores,
-// window 4096, documents: 195 and 257 us.  delta = sum dO O is taken from the
+// window 4096, documents: 199 and 232 us.  delta = sum dO O is taken from the
 // bf16 O that the caller holds.
 #include "attn_common.hpp"
 
@@ -188,19 +188,27 @@ done:
 // them.  32 queries are one block of a tile; as above
 //     products   S, dP (0)   S, dP (1)   dV, dK (0)   dV, dK (1)
 //     vector                 block 0     block 1
-template <int DP, int NW, int MOD>
-__global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const AttnArgs) {
-    constexpr int BN = 32 * NW, NT = 64 * NW, TB = 2 * Tile<DP>::ELEMS;
+// PAIR: two waves share 32 keys.  Each makes P and dS of one block of a tile
+// and hands them to the other (they are operands as they lie, so the other's
+// lanes read them back unchanged), and each sums half of the columns of dV and
+// dK over both blocks: the same products, with half of the accumulators, so
+// two waves fit on a SIMD (heads of 128: 440 registers, 240 as pairs).
+template <int DP, int NW, bool PAIR, int MOD>
+__global__ __launch_bounds__(64 * NW, DP == 64 || PAIR ? 2 : 1) void k_attn_dkv(const AttnArgs) {
+    constexpr int BN = PAIR ? 16 * NW : 32 * NW, NT = 64 * NW, TB = 2 * Tile<DP>::ELEMS;
+    static_assert(!PAIR || DP == 128, "halves of the columns differ in one address bit");
     constexpr int ST = 2;  // one tile lands while the other is used (with three: 1 to 8 % slower)
     __shared__ __align__(16) bf16_t lds[ST][2][Tile<DP>::ELEMS];
     __shared__ __align__(16) float sstat[ST][2][kTile];
     __shared__ __align__(16) int sdocs[ST][kTile];
+    __shared__ __align__(16) bf16x8 handed[PAIR ? NW : 1][PAIR ? 4 : 1][64];
     const Args a = arguments();
     const int U = a->b * a->hkv;
     const int blk = blockIdx.x, u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
     const int j0 = blk / U * BN;
     const Seq seq = sequence(a, b);
-    const int w0 = j0 + wave_id() * 32;
+    const int part = PAIR ? wave_id() & 1 : 0;
+    const int w0 = j0 + (PAIR ? wave_id() >> 1 : wave_id()) * 32;
     auto key_span = [&](int lo, int hi) {
         Span r;
         r.p0 = lo;
@@ -255,9 +263,15 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
     ColFrag<DP> cf;
     rf.init();
     cf.init();
-    f32x16 dk[DP / 32], dv[DP / 32];
+    constexpr int OT = DP / 32 / (PAIR ? 2 : 1);  // this wave's 32 columns of dK and dV
+    if constexpr (PAIR)
 #pragma unroll
-    for (int dt = 0; dt < DP / 32; ++dt) dk[dt] = dv[dt] = splat(0.0f);
+        for (int dt = 0; dt < OT; ++dt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) cf.off[dt][e] ^= DP * part;
+    f32x16 dk[OT], dv[OT];
+#pragma unroll
+    for (int dt = 0; dt < OT; ++dt) dk[dt] = dv[dt] = splat(0.0f);
     settle(kf);
     settle(vf);
 
@@ -333,6 +347,77 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
             in_order();
         });
     };
+    auto share = [&](uint32_t tq, uint32_t td, const float* sl, const float* sdel, const int* sdoc, int seen, const Score& score, int q0) {
+        // this wave's block is `part`
+        const int h4 = 4 * (lane_id() >> 5), r0 = 32 * part + h4;
+        constexpr int kRing = 4;
+        bf16x8 ring[kRing], p[4];
+        auto across = [&](int y, int block) {  // dO and Q in turn, 2 steps of OT column tiles
+            return cf.read((y % 2 ? tq : td) + 64 * block * Tile<DP>::LD, y / 2 / OT, y / 2 % OT);
+        };
+        auto products = [&](int block) {
+            each<0, kRing>([&](auto y) { ring[y.value] = across(y.value, block); });
+            in_order();
+            each<0, 4 * OT>([&](auto y_) {
+                constexpr int y = decltype(y_)::value, dt = y / 2 % OT, t = y / 2 / OT;
+                if constexpr (y % 2 == 0) dv[dt] = mfma(ring[y % kRing], p[t], dv[dt]);
+                else dk[dt] = mfma(ring[y % kRing], p[2 + t], dk[dt]);
+                if constexpr (y + kRing < 4 * OT) ring[y % kRing] = across(y + kRing, block);
+                in_order();
+            });
+        };
+        if (seen) {
+            f32x16 s, dp;
+            each<0, 16>([&](auto i_) {
+                constexpr int i = decltype(i_)::value;
+                s[i] = MOD ? 0.0f : sl[r0 + place(i)];
+                dp[i] = sdel[r0 + place(i)];
+            });
+            auto along = [&](int y) { return rf.read((y % 2 ? td : tq) + 64 * part * Tile<DP>::LD, 0, y / 2); };
+            each<0, kRing>([&](auto y) { ring[y.value] = along(y.value); });
+            in_order();
+            each<0, 2 * KT>([&](auto y_) {
+                constexpr int y = decltype(y_)::value;
+                if constexpr (y % 2 == 0) s = mfma(ring[y % kRing], kf[y / 2], s);
+                else dp = mfma(ring[y % kRing], vf[y / 2], dp);
+                if constexpr (y + kRing < 2 * KT) ring[y % kRing] = along(y + kRing);
+                in_order();
+            });
+            each<0, 16>([&](auto i_) {
+                constexpr int i = decltype(i_)::value;
+                grad1<MOD, true>(score, s, dp, i, MOD ? sl[r0 + place(i)] : 0.0f,
+                                 fabsf(static_cast<float>(seq.start + q0 + r0 - col.pos) + static_cast<float>(place(i))));
+            });
+            if (seen == 1 || !whole) {
+                const int p0 = seq.start + q0 + r0;
+                const Bits m = bits_of(col.lo - p0, col.hi - p0, 0);
+                each<0, 16>([&](auto i) {
+                    s[i.value] = where(m, 0, i.value, s[i.value], 0.0f);
+                    dp[i.value] = where(m, 0, i.value, dp[i.value], 0.0f);
+                });
+                if (sdoc)
+                    each<0, 16>([&](auto i_) {
+                        constexpr int i = decltype(i_)::value;
+                        const bool mine = sdoc[r0 + place(i)] == col.doc;
+                        s[i] = mine ? s[i] : 0.0f;
+                        dp[i] = mine ? dp[i] : 0.0f;
+                    });
+            }
+            p[0] = pack(s, 0);
+            p[1] = pack(s, 1);
+            p[2] = pack(dp, 0);
+            p[3] = pack(dp, 1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) handed[wave_id()][e][lane_id()] = p[e];
+            products(part);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (seen) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = handed[wave_id() ^ 1][e][lane_id()];
+            products(1 - part);
+        }
+    };
     // (the two buffers' code side by side: as one loop, 3 to 25 % slower)
     for (;;) {
 #pragma unroll
@@ -340,7 +425,10 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 2 : 1) void k_attn_dkv(const At
             if (tile[x] < 0) goto done;
             landed();
             fetch(1 - x);
-            if (mode[x] != 0)
+            if constexpr (PAIR)
+                share(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x], sc[x],
+                      tile[x] * kTile);
+            else if (mode[x] != 0)
                 step(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x] == 1 || !whole, sc[x],
                      tile[x] * kTile);
         }
@@ -349,8 +437,8 @@ done:
     const Args z = again(a);
     // dk and dv are contiguous (b, sk, hkv, d)
     const int64_t to = ((static_cast<int64_t>(b) * z->sk + j) * z->hkv + kvh) * z->d;
-    store_rows<DP>(dk, z->scale, z->dk + to, j < z->sk, z->d);
-    store_rows<DP>(dv, 1.0f, z->dv + to, j < z->sk, z->d);
+    store_rows<32 * OT>(dk, z->scale, z->dk + to + 32 * OT * part, j < z->sk, z->d - 32 * OT * part);
+    store_rows<32 * OT>(dv, 1.0f, z->dv + to + 32 * OT * part, j < z->sk, z->d - 32 * OT * part);
 }
 
 template <int DP, int MOD>
@@ -361,9 +449,14 @@ void dq(const AttnArgs& a, hipStream_t stream) {
 }
 template <int DP, int MOD>
 void dkv(const AttnArgs& a, hipStream_t stream) {
-    constexpr int NW = 4, BN = 32 * NW;
+    constexpr int BN = 128;
     const int blocks = (a.sk + BN - 1) / BN * a.b * a.hkv;
-    k_attn_dkv<DP, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    // pairs where the cap makes the vector work long enough to hide the
+    // handing over: capped documents of 16384 tokens 258 -> 232 us, capped 2 x
+    // 2048 tokens of 12 heads (both kernels) 160 -> 155; without a cap 16 x 1024
+    // tokens of 6 heads 151 -> 159, 4 x 4096 of 16 heads over 4 945 -> 975
+    if constexpr (DP == 128 && (MOD & kCap) != 0) k_attn_dkv<DP, 8, true, MOD><<<blocks, 512, 0, stream>>>(a);
+    else k_attn_dkv<DP, 4, false, MOD><<<blocks, 256, 0, stream>>>(a);
 }
 
 }  // namespace
