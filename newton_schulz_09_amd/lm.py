@@ -76,8 +76,19 @@ def _last(t, name):
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
+def _heads(t, name, dev):
+    """bfloat16 of 4 dimensions on `dev`, the last one contiguous."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.is_cuda and t.device == dev and t.dim() == 4
+            and t.stride(3) == 1):
+        _tensor(t, name, _BF16, dev, 4)
+        _last(t, name)
+
+
 def _exactly(t, name, dtype, dev, shape):
     """A contiguous tensor of one shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.device == dev and t.shape == shape
+            and t.is_contiguous()):
+        return
     _tensor(t, name, dtype, dev)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
@@ -113,9 +124,9 @@ def _attention_args(q, k, v, out, lse, dout, grads, scale, causal, window, softc
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
     dev = q.device
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        _tensor(t, name, _BF16, dev, 4)
-        _last(t, name)
+    _heads(q, "q", dev)
+    _heads(k, "k", dev)
+    _heads(v, "v", dev)
     b, sq, hq, d = q.shape
     kb, sk, hkv, kd = k.shape
     if kb != b or kd != d or v.shape != k.shape:
@@ -151,8 +162,7 @@ def _attention_args(q, k, v, out, lse, dout, grads, scale, causal, window, softc
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
-        _tensor(out, "out", _BF16, dev, 4)
-        _last(out, "out")
+        _heads(out, "out", dev)
         if out.shape != q.shape:
             raise ValueError(f"out must have q's shape {tuple(q.shape)} (got {tuple(out.shape)})")
     if lse is None:
@@ -208,8 +218,7 @@ def attention_backward(dout, q, k, v, out, lse, scale=None, causal=True, window=
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
     dev = q.device
-    _tensor(dout, "dout", _BF16, dev, 4)
-    _last(dout, "dout")
+    _heads(dout, "dout", dev)
     if out is None or lse is None:
         raise TypeError("out and lse of the forward pass are needed")
     if dout.shape != q.shape:

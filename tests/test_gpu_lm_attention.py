@@ -257,3 +257,39 @@ def test_nan_at_keys_that_are_masked_but_never_read(lm):
     k[:, 90:] = float("nan")
     got = lm.attention(q, k, v)[0]
     assert torch.equal(got[:, :90], clean) and torch.isnan(got[:, 90:]).all()
+
+
+def test_refusals_of_the_binding(lm):
+    """Nothing here reaches a kernel."""
+    q, k, v, dout = make(2, 40, 50, 4, 2, 64)
+    out, lse = lm.attention(q, k, v)
+    i = ints(1, 2)
+    for e, fn in (
+            (TypeError, lambda: lm.attention(q.float(), k, v)), (TypeError, lambda: lm.attention(q, k.half(), v)),
+            (ValueError, lambda: lm.attention(q, k.cpu(), v)), (ValueError, lambda: lm.attention(q[0], k, v)),
+            (ValueError, lambda: lm.attention(q, k, v[:, :49])), (ValueError, lambda: lm.attention(q[:1], k, v)),
+            (ValueError, lambda: lm.attention(q[..., :32], k, v)), (ValueError, lambda: lm.attention(q[:, :, :3], k, v)),
+            (ValueError, lambda: lm.attention(q.transpose(2, 3), k, v)), (TypeError, lambda: lm.attention(q, None, v)),
+            (ValueError, lambda: lm.attention(*(t[..., :12].contiguous() for t in (q, k, v)))),
+            (ValueError, lambda: lm.attention(q, k, v, slopes=torch.ones(3).cuda())),
+            (TypeError, lambda: lm.attention(q, k, v, lengths=i.long())),
+            (ValueError, lambda: lm.attention(q, k, v, starts=i[:1])),
+            (ValueError, lambda: lm.attention(q, k, v, prefix=i.cpu())),
+            (ValueError, lambda: lm.attention(q, k, v, documents=torch.zeros(2, 40, dtype=torch.int32).cuda())),
+            (ValueError, lambda: lm.attention(q, k, v, out=out[:, :39])),
+            (ValueError, lambda: lm.attention(q, k, v, lse=lse.transpose(1, 2))),
+            (ValueError, lambda: lm.attention(q, k, v, workspace=torch.zeros(512, dtype=torch.uint8))),
+            (RuntimeError, lambda: lm.attention(q, k, v, workspace=torch.zeros(16, dtype=torch.uint8).cuda())),
+            (RuntimeError, lambda: lm.attention(q, k, v, scale=-1.0)),
+            (RuntimeError, lambda: lm.attention(q, k, v, window=-1)),
+            (RuntimeError, lambda: lm.attention(q, k, v, softcap=float("nan"))),
+            (TypeError, lambda: lm.attention_backward(dout, q, k, v, None, lse)),
+            (TypeError, lambda: lm.attention_backward(dout.float(), q, k, v, out, lse)),
+            (ValueError, lambda: lm.attention_backward(dout[:, :39], q, k, v, out, lse)),
+            (ValueError, lambda: lm.attention_backward(dout, q, k, v, out, lse[:, :3])),
+            (ValueError, lambda: lm.attention_backward(dout, q, k, v, out, lse, dk=torch.empty_like(q)))):
+        with pytest.raises(e):
+            fn()
+    wide = torch.zeros(2, 40, 4, 65, dtype=torch.bfloat16, device="cuda")[..., :64]  # rows that are not aligned
+    with pytest.raises(RuntimeError):
+        lm.attention(wide, k, v)
