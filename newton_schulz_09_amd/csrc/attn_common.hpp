@@ -94,14 +94,17 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // Direct loads from memory to LDS: lane l's 16 (4) bytes land at lds + 16 l
 // (4 l).  In asm, because the compiler cannot tell which LDS reads such a
 // load in flight concerns and would wait for it before every one; the loads
-// have no result registers, and landed() orders them.
+// have no result registers, and landed() orders them.  The wait states are
+// those between a lane instruction's write of a scalar register (the
+// descriptor) and a memory instruction that reads it, 5, which the compiler
+// counts only for its own instructions; m0 needs 1.
 __device__ __forceinline__ void load_lds16(uint32_t lds, uint32_t voff, u32x4 desc) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
-                 : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds4(uint32_t lds, uint32_t voff, u32x4 desc) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
-                 : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(voff), "s"(desc)
+                 : "memory", "m0");
 }
 // This wave's loads have landed and its LDS reads are done, and so for every
 // wave of the workgroup.
