@@ -293,3 +293,26 @@ def test_refusals_of_the_binding(lm):
     wide = torch.zeros(2, 40, 4, 65, dtype=torch.bfloat16, device="cuda")[..., :64]  # rows that are not aligned
     with pytest.raises(RuntimeError):
         lm.attention(wide, k, v)
+
+
+@pytest.mark.parametrize("sq", [1, 70, 300])
+def test_offsets_past_32_bits(lm, sq):
+    """Keys and values whose rows lie 2^21 elements apart: 8.8 GB from first to last."""
+    sk, step = 2100, 2 ** 21
+    flat = torch.empty(sk * step, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(4)
+    views = [flat.as_strided((1, sk, 2, 64), (0, step, 64, 1), off) for off in (0, 128)]
+    for t in views:
+        t.copy_(torch.randn(1, sk, 2, 64, generator=g).bfloat16())
+    q, dout = (torch.randn(1, sq, 4, 64, generator=g).bfloat16().cuda() for _ in range(2))
+    check(lm, q, *views, dout, backward=sq == 300, window=500)
+
+
+def test_offsets_of_batches_past_32_bits(lm):
+    b, s, step = 3, 140, 2 ** 31
+    flat = torch.empty((b - 1) * step + s * 128, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(5)
+    x = flat.as_strided((b, s, 2, 64), (step, 128, 64, 1))
+    x.copy_(torch.randn(b, s, 2, 64, generator=g).bfloat16())
+    dout = torch.randn(b, s, 2, 64, generator=g).bfloat16().cuda()
+    check(lm, x, x, x, dout)

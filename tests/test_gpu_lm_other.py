@@ -217,3 +217,31 @@ def test_embedding_gradient_at_the_borders_of_its_variants(lm, n, vocab, width):
     tokens = (torch.rand(n, generator=g, dtype=torch.float64) ** 3 * vocab).long()
     check_embed(lm, tokens.cuda(), vocab, width, torch.bfloat16, torch.bfloat16, 1.0)
     check_embed(lm, tokens.int().cuda(), vocab, width, torch.float32, torch.bfloat16, 0.5)
+
+
+@pytest.mark.parametrize("n", [5, 3000])
+def test_embedding_offsets_past_32_bits(lm, n):
+    """A table of 2.3e9 elements (4.6 GB)."""
+    vocab, width = 70000, 32768
+    table = torch.empty(vocab, width, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator().manual_seed(6)
+    rows = torch.tensor([0, 1, 65535, 65536, 65537, 69999]).cuda()
+    table[rows] = torch.randn(6, width, generator=g).bfloat16().cuda()
+    tokens = rows[torch.randint(0, 6, (n,), generator=g).cuda()]
+    assert torch.equal(lm.embedding(tokens, table), table[tokens])
+    dout = torch.randint(-3, 4, (n, width), generator=g).bfloat16().cuda()  # sums of whole numbers are exact
+    table.fill_(7.0)
+    lm.embedding_backward(dout, tokens, vocab, dtype=torch.bfloat16, out=table)
+    for r in rows.tolist():
+        want = dout[tokens == r].float().sum(0).bfloat16()
+        assert torch.equal(table[r], want), r
+    assert int((table != 0).any(1).sum()) <= 6
+
+
+def test_norm_offsets_past_32_bits(lm):
+    b, s, step = 3, 9, 2 ** 31
+    flat = torch.empty((b - 1) * step + s * 128, dtype=torch.bfloat16, device="cuda")
+    q, k, qw, kw, dq, dk, pos = qk_inputs(b, s, 2, 1, 64, torch.bfloat16)
+    x = flat.as_strided((b, s, 2, 64), (step, 128, 64, 1))
+    x.copy_(q)
+    check_qk(lm, x, k, qw, kw, dq, dk, pos, table(64), True)
