@@ -7,7 +7,7 @@
 // 16 x 1024 tokens of 12 heads of 64, causal: dQ 61 us, dK and dV 72, both bound
 // by vector work (an exponential and 4 other instructions a score) and its
 // waits.  One packed sequence of 16384 tokens, 6 heads of 128, capped scores,
-// window 4096, documents: 199 and 232 us.  delta = sum dO O is taken from the
+// window 4096, documents: 190 and 224 us.  delta = sum dO O is taken from the
 // bf16 O that the caller holds.
 #include "attn_common.hpp"
 
@@ -17,26 +17,44 @@ namespace {
 
 using namespace attn;
 
-// Result i of a block: s holds q . k (LSE: minus lse already, in the product's
-// units; else lse2 is subtracted, in units of log 2), dp holds dO . v - delta;
-// they become P and dS.
+// Result i of a block: s holds q . k, dp holds dO . v - delta; they become P
+// and dS, with a cap a quarter of dS (dQ and dK are scaled by 4 at the end).
+// term: what is subtracted from the scores in units of log 2, lse or with a cap
+// lse minus the cap; LSE: the products started from -lse, nothing is left to do.
+// With the cap's r = 1 / (exp(2 y) + 1): score = cap - 2 cap r, derivative 4 (r - r^2).
 template <int MOD, bool LSE>
-__device__ __forceinline__ void grad1(const Score& sc, f32x16& s, f32x16& dp, int i, float lse2, float dist) {
-    float r = 0.0f;
-    const float p = exp2_fast(MOD ? score<MOD>(sc, s[i], dist, r) - lse2 : (LSE ? s[i] * sc.c : fmaf(s[i], sc.c, -lse2)));
+__device__ __forceinline__ void grad1(const Score& sc, f32x16& s, f32x16& dp, int i, float term, float dist) {
+    float z, r = 0.0f;
+    if constexpr (MOD & kCap) {
+        r = __builtin_amdgcn_rcpf(exp2_fast(s[i] * sc.c) + 1.0f);
+        z = fmaf(-2.0f * sc.a, r, -term);
+    } else {
+        z = LSE && MOD == 0 ? s[i] * sc.c : fmaf(s[i], sc.c, -term);
+    }
+    if constexpr (MOD & kBias) z = fmaf(-sc.slope, dist, z);
+    const float p = exp2_fast(z);
     float ds = p * dp[i];
-    if constexpr (MOD & kCap) ds *= 4.0f * fmaf(-r, r, r);
+    if constexpr (MOD & kCap) ds *= fmaf(-r, r, r);
     s[i] = p;
     dp[i] = ds;
 }
 
-// What the second kernel subtracts from a row's scores: with extras lse in
-// units of log 2, +inf for a row that saw nothing (its P is then zero);
-// without, -lse in units of the product q . k, where its products start.
+// grad1's term of a row; +inf for one that saw nothing (its P is then zero).
 template <int MOD>
-__device__ __forceinline__ float lse_term(float lse, float scale) {
-    if constexpr (MOD != 0) return lse == neg_inf() ? __builtin_inff() : lse * kLog2e;
+__device__ __forceinline__ float row_term(float lse, const Score& sc) {
+    if (lse == neg_inf()) return __builtin_inff();
+    return (MOD & kCap) ? fmaf(lse, kLog2e, -sc.a) : lse * kLog2e;
+}
+// The second kernel's: without extras -lse in units of the product q . k, where
+// its products start.
+template <int MOD>
+__device__ __forceinline__ float start_term(float lse, const Score& sc, float scale) {
+    if constexpr (MOD != 0) return row_term<MOD>(lse, sc);
     else return lse == neg_inf() ? neg_inf() : -lse / scale;
+}
+template <int MOD>
+__device__ __forceinline__ float grad_scale(float scale) {
+    return (MOD & kCap) ? 4.0f * scale : scale;
 }
 
 // dQ.  32 keys are one block; the gradients of the scores of a block are made
@@ -97,10 +115,10 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
     }
     const int64_t stat = (static_cast<int64_t>(b) * a->hq + h) * a->sq + i;
     const float given = real ? a->lse[stat] : neg_inf();
-    const float lse2 = given == neg_inf() ? __builtin_inff() : given * kLog2e;
+    const float term = row_term<MOD>(given, sc);
     if (i < a->sq && lane_id() < 32) {
         // for the second kernel: what it starts its products from
-        a->stats[stat] = lse_term<MOD>(given, a->scale);
+        a->stats[stat] = start_term<MOD>(given, sc, a->scale);
         a->stats[stat + a->delta_at] = -delta;
     }
     RowFrag<DP> rf;
@@ -125,7 +143,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
                               : cf.read(tk, (y - 4 * KT) / DT, (y - 4 * KT) % DT);
         };
         auto grads = [&](int kb, int i) {
-            grad1<MOD, false>(sc, s[kb], dp[kb], i, lse2,
+            grad1<MOD, false>(sc, s[kb], dp[kb], i, term,
                        fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + place(i))));
         };
         auto finish = [&](int kb) {
@@ -181,7 +199,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
 done:
     const Args z = again(a);
     // dq is contiguous (b, sq, hq, d)
-    store_rows<DP>(dq, z->scale, z->dq + ((static_cast<int64_t>(b) * z->sq + i) * z->hq + h) * z->d, i < z->sq, z->d);
+    store_rows<DP>(dq, grad_scale<MOD>(z->scale), z->dq + ((static_cast<int64_t>(b) * z->sq + i) * z->hq + h) * z->d, i < z->sq, z->d);
 }
 
 // dK and dV of 32 NW keys, walked over the queries of every head that shares
@@ -437,7 +455,7 @@ done:
     const Args z = again(a);
     // dk and dv are contiguous (b, sk, hkv, d)
     const int64_t to = ((static_cast<int64_t>(b) * z->sk + j) * z->hkv + kvh) * z->d;
-    store_rows<32 * OT>(dk, z->scale, z->dk + to + 32 * OT * part, j < z->sk, z->d - 32 * OT * part);
+    store_rows<32 * OT>(dk, grad_scale<MOD>(z->scale), z->dk + to + 32 * OT * part, j < z->sk, z->d - 32 * OT * part);
     store_rows<32 * OT>(dv, 1.0f, z->dv + to + 32 * OT * part, j < z->sk, z->d - 32 * OT * part);
 }
 
