@@ -615,8 +615,7 @@ struct QueryTiles {
 
 // Scores in units of log 2 from the product x = q . k, as p = exp2(z - lse2).
 // cap: z = cap log2e tanh(scale x / cap), with tanh(y) = 1 - 2 / (exp(2 y) +
-// 1), exact to float32 rounding at both ends; r = 1 / (exp(2 y) + 1) gives the
-// derivative 1 - tanh^2 = 4 (r - r^2).
+// 1), exact to float32 rounding at both ends.
 struct Score {
     float c;      // scale * log2e (no cap) or 2 scale log2e / cap
     float a;      // cap * log2e
@@ -630,12 +629,12 @@ __device__ __forceinline__ Score score_of(Args a, int head) {
     s.slope = (MOD & kBias) ? a->slopes[head] * kLog2e : 0.0f;
     return s;
 }
-// dist: |query position - key|.  r receives 1 / (exp(2 y) + 1).
+// dist: |query position - key|.
 template <int MOD>
-__device__ __forceinline__ float score(const Score& s, float x, float dist, float& r) {
+__device__ __forceinline__ float score(const Score& s, float x, float dist) {
     float z;
     if constexpr (MOD & kCap) {
-        r = __builtin_amdgcn_rcpf(exp2_fast(x * s.c) + 1.0f);
+        const float r = __builtin_amdgcn_rcpf(exp2_fast(x * s.c) + 1.0f);
         z = fmaf(-2.0f * s.a, r, s.a);
     } else {
         z = x * s.c;

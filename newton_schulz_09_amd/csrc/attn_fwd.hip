@@ -53,9 +53,8 @@ __device__ __forceinline__ void tile_step(Running<DP>& run, const bf16x8 (&qf)[D
     bf16x8 p[4], ring[kAhead];
     f32x16 s[2];
     auto extras = [&](int kb, int i) {
-        float r;
         const float dist = fabsf(static_cast<float>(row.pos - k0 - h4) - static_cast<float>(32 * kb + place(i)));
-        s[kb][i] = score<MOD>(sc, s[kb][i], dist, r);
+        s[kb][i] = score<MOD>(sc, s[kb][i], dist);
     };
     auto operand = [&](int x) {  // of product x: keys along the row, then V across
         return x < 2 * KT ? rf.read(sk, x / KT, x % KT) : cf.read(sv, (x - 2 * KT) / DT, (x - 2 * KT) % DT);
