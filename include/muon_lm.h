@@ -56,7 +56,9 @@ extern "C" {
  *
  * Scores, statistics and sums are float32.  exp(z - lse) and the gradient of
  * the scores are rounded to bfloat16 as operands of the matrix cores; the
- * backward pass takes sum dout out from the rounded out it is given.
+ * backward pass takes sum dout out from the rounded out it is given.  A capped
+ * score is good to 2^-22 of the cap up to a cap of 64, and to 2^-19 of itself
+ * above.
  */
 typedef struct muon_attention_args {
     const uint16_t *q;      /* [batch][sq][heads][d], bfloat16 */

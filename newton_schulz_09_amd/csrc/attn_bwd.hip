@@ -19,13 +19,16 @@ using namespace attn;
 
 // Result i of a block: s holds q . k, dp holds dO . v - delta; they become P
 // and dS, with a cap a quarter of dS (dQ and dK are scaled by 4 at the end).
-// term: what is subtracted from the scores in units of log 2, lse or with a cap
-// lse minus the cap; LSE: the products started from -lse, nothing is left to do.
-// With the cap's r = 1 / (exp(2 y) + 1): score = cap - 2 cap r, derivative 4 (r - r^2).
+// term: what is subtracted from the scores in units of log 2, lse or with a
+// cap up to kMaxPlainCap lse minus the cap; LSE: the products started from -lse,
+// nothing is left to do.  With the cap's r = 1 / (exp(2 y) + 1): score = cap - 2
+// cap r, derivative 4 (r - r^2), which is exact near zero too.
 template <int MOD, bool LSE>
 __device__ __forceinline__ void grad1(const Score& sc, f32x16& s, f32x16& dp, int i, float term, float dist) {
     float z, r = 0.0f;
-    if constexpr (MOD & kCap) {
+    if constexpr (MOD & kWide) {
+        z = capped<MOD>(sc, s[i], r) - term;
+    } else if constexpr (MOD & kCap) {
         r = __builtin_amdgcn_rcpf(exp2_fast(s[i] * sc.c) + 1.0f);
         z = fmaf(-2.0f * sc.a, r, -term);
     } else {
@@ -43,7 +46,7 @@ __device__ __forceinline__ void grad1(const Score& sc, f32x16& s, f32x16& dp, in
 template <int MOD>
 __device__ __forceinline__ float row_term(float lse, const Score& sc) {
     if (lse == neg_inf()) return __builtin_inff();
-    return (MOD & kCap) ? fmaf(lse, kLog2e, -sc.a) : lse * kLog2e;
+    return (MOD & kCap) && !(MOD & kWide) ? fmaf(lse, kLog2e, -sc.a) : lse * kLog2e;
 }
 // The second kernel's: without extras -lse in units of the product q . k, where
 // its products start.

@@ -41,9 +41,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxPos = 1 << 29;
 
-// Extras of the scores, as template bits.
+// Extras of the scores, as template bits.  kWide: a cap above kMaxPlainCap (with
+// kCap and kBias; the slope is 0 where none is given).
 constexpr int kCap = 1;
 constexpr int kBias = 2;
+constexpr int kWide = 4;
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -614,33 +616,57 @@ struct QueryTiles {
 };
 
 // Scores in units of log 2 from the product x = q . k, as p = exp2(z - lse2).
-// cap: z = cap log2e tanh(scale x / cap), with tanh(y) = 1 - 2 / (exp(2 y) +
-// 1), exact to float32 rounding at both ends.
+// cap: z = cap log2e tanh(scale x / cap), with tanh(y) = 1 - 2 r, r = 1 / (exp(2
+// y) + 1).  That is exact to float32 rounding of the cap, not of the score: near
+// zero r is 1/2 and the score what is left of the difference, off by about 2^-23
+// of the cap (6e-6 at 30, 1.3e-5 at 64, but 0.01 at 1e5).  Above kMaxPlainCap
+// scores below a quarter of the cap are taken from the series y - y^3 / 3 + 2
+// y^5 / 15 - ..., whose first term left out is 9e-9 of the sum there; packed
+// documents of 16384 tokens take 219 us forward and 512 backward so, and 162 and
+// 387 up to it; a step over 32 caches of up to 16384 keys 296 and 288.
+constexpr float kMaxPlainCap = 64.0f;
 struct Score {
     float c;      // scale * log2e (no cap) or 2 scale log2e / cap
     float a;      // cap * log2e
     float slope;  // slope * log2e
+    float line, over;  // kWide: scale * log2e, scale / cap
 };
 template <int MOD>
 __device__ __forceinline__ Score score_of(Args a, int head) {
+    // (a product past float32's range is that range's end: 0 times it is 0)
+    constexpr float most = 3.4028234663852886e38f;
     Score s;
-    s.a = a->softcap * kLog2e;
-    s.c = (MOD & kCap) ? 2.0f * a->scale * kLog2e / a->softcap : a->scale * kLog2e;
-    s.slope = (MOD & kBias) ? a->slopes[head] * kLog2e : 0.0f;
+    s.a = fminf(a->softcap * kLog2e, most);
+    s.line = fminf(a->scale * kLog2e, most);
+    s.c = (MOD & kCap) ? fminf(2.0f * (s.line / a->softcap), most) : s.line;
+    s.over = a->scale / a->softcap;
+    s.slope = (MOD & kBias) && a->slopes ? a->slopes[head] * kLog2e : 0.0f;
     return s;
+}
+// The capped score of x without a bias, and r.
+template <int MOD>
+__device__ __forceinline__ float capped(const Score& s, float x, float& r) {
+    r = __builtin_amdgcn_rcpf(exp2_fast(x * s.c) + 1.0f);
+    if constexpr (!(MOD & kWide)) return fmaf(-2.0f * s.a, r, s.a);
+    const float y = x * s.over, w = y * y;
+    const float near = fmaf(w * fmaf(w, fmaf(w, fmaf(w, 62.0f / 2835.0f, -17.0f / 315.0f), 2.0f / 15.0f), -1.0f / 3.0f),
+                            x * s.line, x * s.line);
+    return w < 0.0625f ? near : s.a * fmaf(-2.0f, r, 1.0f);
 }
 // dist: |query position - key|.
 template <int MOD>
 __device__ __forceinline__ float score(const Score& s, float x, float dist) {
-    float z;
-    if constexpr (MOD & kCap) {
-        const float r = __builtin_amdgcn_rcpf(exp2_fast(x * s.c) + 1.0f);
-        z = fmaf(-2.0f * s.a, r, s.a);
-    } else {
-        z = x * s.c;
-    }
+    float z, r;
+    if constexpr (MOD & kCap) z = capped<MOD>(s, x, r);
+    else z = x * s.c;
     if constexpr (MOD & kBias) z = fmaf(-s.slope, dist, z);
     return z;
+}
+
+// The extras of a call.
+inline int score_extras(const AttnArgs& a) {
+    if (a.softcap > kMaxPlainCap) return kCap | kBias | kWide;
+    return (a.softcap > 0.0f ? kCap : 0) | (a.slopes ? kBias : 0);
 }
 
 }  // namespace attn
@@ -649,20 +675,23 @@ __device__ __forceinline__ float score(const Score& s, float x, float dist) {
 // fn<DP, MOD>(a, stream) for the head size and the extras of the scores
 #define MUON_ATTN_DISPATCH(fn, a, stream)                                                     \
     do {                                                                                      \
-        const int mod = ((a).softcap > 0.0f ? kCap : 0) | ((a).slopes ? kBias : 0);           \
+        const int mod = score_extras(a);                                                      \
         const int size = (a).d <= 64 ? 64 : ((a).d <= 96 ? 96 : 128);                         \
         switch (size + mod) {                                                                 \
             case 64: fn<64, 0>(a, stream); break;                                             \
             case 65: fn<64, 1>(a, stream); break;                                             \
             case 66: fn<64, 2>(a, stream); break;                                             \
             case 67: fn<64, 3>(a, stream); break;                                             \
+            case 71: fn<64, 7>(a, stream); break;                                             \
             case 96: fn<96, 0>(a, stream); break;                                             \
             case 97: fn<96, 1>(a, stream); break;                                             \
             case 98: fn<96, 2>(a, stream); break;                                             \
             case 99: fn<96, 3>(a, stream); break;                                             \
+            case 103: fn<96, 7>(a, stream); break;                                            \
             case 128: fn<128, 0>(a, stream); break;                                           \
             case 129: fn<128, 1>(a, stream); break;                                           \
             case 130: fn<128, 2>(a, stream); break;                                           \
             case 131: fn<128, 3>(a, stream); break;                                           \
+            case 135: fn<128, 7>(a, stream); break;                                           \
         }                                                                                     \
     } while (0)
