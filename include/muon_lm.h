@@ -13,6 +13,9 @@
  *    captured into a graph.
  *  - Arguments are validated before anything is enqueued: a non-zero status
  *    enqueues nothing, and muon_last_error() describes it.
+ *  - What a call writes, the workspace included, must not overlap anything it
+ *    reads or writes besides, unless its comment allows that, and elements of
+ *    one output must not overlap; the library does not check it.
  *  - The same inputs give the same bits every time: no sum depends on the
  *    order in which workgroups run.
  *  - Values on the device (lengths, positions, tokens, ...) cannot be checked
@@ -89,7 +92,7 @@ size_t muon_attention_workspace_size(const muon_attention_args *args);
 size_t muon_attention_backward_workspace_size(const muon_attention_args *args);
 
 /*
- * out and lse from q, k and v.
+ * out and lse from q, k and v.  out may be q (the same pointer and strides).
  * Errors: MUON_ERR_INVALID_ARG (null pointers, negative sizes, heads not a
  * multiple of kv_heads, misaligned pointers or strides, a scale that is not
  * positive and finite, a negative softcap or window), MUON_ERR_UNSUPPORTED (d
@@ -98,7 +101,9 @@ size_t muon_attention_backward_workspace_size(const muon_attention_args *args);
  */
 int muon_attention(const muon_attention_args *args, void *workspace, size_t workspace_bytes, void *stream);
 
-/* dq, dk and dv from dout, the forward pass's arguments and its out and lse. */
+/* dq, dk and dv from dout, the forward pass's arguments and its out and lse.
+ * dq may be out, and dk and dv may be k and v (one each), where those are
+ * contiguous too.  dq is written before q and dout are read for dk and dv. */
 int muon_attention_backward(const muon_attention_args *args, void *workspace, size_t workspace_bytes, void *stream);
 
 /*
@@ -107,7 +112,8 @@ int muon_attention_backward(const muon_attention_args *args, void *workspace, si
  *   z = (a cos - b sin, b cos + a sin)
  * with (cos, sin) = table[position][pair].  Computed in float32 and rounded
  * once.  Index 0 of each pair of fields is the queries', 1 the keys'.
- * Positions outside the table give NaN.
+ * Positions outside the table give NaN.  out[i] may be x[i] (backward: dz[i]
+ * too) where that is contiguous.
  */
 typedef struct muon_qk_norm_rope_args {
     const void *x[2];       /* [batch][positions][heads[i]][d] of dtype */

@@ -96,6 +96,75 @@ def _exactly(t, name, dtype, dev, shape):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _layout(t):
+    """(first byte, past the last one, bytes of a contiguous piece, steps
+    between pieces) of a tensor that has elements."""
+    size = t.element_size()
+    end = piece = size
+    steps = []
+    for step, n in sorted(zip(t.stride(), t.shape)):
+        if n > 1:
+            end += (n - 1) * step * size
+            if step * size == piece and not steps:
+                piece *= n
+            elif step:
+                steps.append(step * size)
+    at = t.data_ptr()
+    return at, at + end, piece, steps
+
+
+def _end(t):
+    """Past a tensor's last byte."""
+    if t.is_contiguous():
+        return t.data_ptr() + t.nbytes
+    return _layout(t)[1]
+
+
+def _overlap(a, b):
+    """Whether two tensors may share memory: never False where they do."""
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    a0, a1, piece, steps = _layout(a)
+    if b.data_ptr() >= a1:
+        return False
+    b0, b1, other, more = _layout(b)
+    if b1 <= a0:
+        return False
+    # interleaved (heads of one projection): pieces begin at multiples of the
+    # steps' divisor, those of b `off` past those of a
+    step = math.gcd(*steps, *more)
+    if step == 0:
+        return True
+    off = (b0 - a0) % step
+    return off < piece or off + other > step
+
+
+def _repeats(t):
+    """Whether elements of a tensor may share memory."""
+    end = 1
+    for step, n in sorted(zip(t.stride(), t.shape)):
+        if n > 1:
+            if step < end:
+                return True
+            end += (n - 1) * step
+    return False
+
+
+def _apart(t, name, *others):
+    """Refuses a given output that shares memory with a tensor the kernels read
+    beside it; others: (tensor or None, name), and True for one that may be
+    the output itself, element for element."""
+    first = t.data_ptr()
+    end = _end(t)
+    for o, other, *itself in others:
+        if o is None or o.data_ptr() >= end or _end(o) <= first or not _overlap(t, o):
+            continue
+        if itself and t.data_ptr() == o.data_ptr() and t.shape == o.shape and all(
+                x == y or n == 1 for x, y, n in zip(t.stride(), o.stride(), t.shape)):
+            continue
+        raise ValueError(f"{name} must not share memory with {other}")
+
+
 def _ws(workspace, need, dev):
     """(address, bytes) of the caller's workspace or of a new one, and what holds it."""
     if workspace is None:
@@ -199,10 +268,23 @@ def attention(q, k, v, scale=None, causal=True, window=0, softcap=0.0, slopes=No
       or not; ``lengths`` (batch,) int32: positions from there on are padding,
       as keys and as queries, and may hold anything.
 
+    ``out`` may be q itself; else given outputs must not share memory with
+    anything (nor may elements of ``out`` among themselves).
+
     A query that sees no key gets out = 0 and lse = -inf.  A step of generation
     (up to 32 query rows per key head) reads each cached key and value once."""
+    given = out, lse
     args, out, lse, dev = _attention_args(q, k, v, out, lse, None, (0, 0, 0), scale, causal, window, softcap, slopes,
                                           documents, prefix, lengths, starts)
+    if given[0] is not None or given[1] is not None:
+        reads = ((k, "k"), (v, "v"), (slopes, "slopes"), (documents, "documents"), (prefix, "prefix"),
+                 (lengths, "lengths"), (starts, "starts"))
+        if given[0] is not None:
+            if not out.is_contiguous() and _repeats(out):
+                raise ValueError("elements of out share memory")
+            _apart(out, "out", (q, "q", True), *reads, (given[1], "lse"))
+        if given[1] is not None:
+            _apart(lse, "lse", (q, "q"), *reads)
     ptr, size, ws = _ws(workspace, _lib.muon_attention_workspace_size(args) or 256, dev)
     _call(dev, _lib.muon_attention, args, ptr, size)
     return out, lse
@@ -213,7 +295,10 @@ def attention_backward(dout, q, k, v, out, lse, scale=None, causal=True, window=
                        workspace=None):
     """Gradients ``(dq, dk, dv)`` (bfloat16, contiguous) from ``dout``, the
     gradient of ``out``, and the arguments and results of ``attention``.  The
-    gradients of a shared key head sum over its query heads."""
+    gradients of a shared key head sum over its query heads.  A given dq may be
+    ``out`` itself, dk and dv may be k and v; else given gradients must not
+    share memory with q, k, v, dout, the masks or each other, and dq not with
+    out or lse either."""
     for t, name in ((q, "q"), (k, "k"), (v, "v")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -223,7 +308,7 @@ def attention_backward(dout, q, k, v, out, lse, scale=None, causal=True, window=
         raise TypeError("out and lse of the forward pass are needed")
     if dout.shape != q.shape:
         raise ValueError(f"dout must have q's shape {tuple(q.shape)} (got {tuple(dout.shape)})")
-    grads = []
+    grads, given = [], (dq, dk, dv)
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
         if t is None:
             t = torch.empty_like(like, memory_format=torch.contiguous_format)
@@ -232,6 +317,18 @@ def attention_backward(dout, q, k, v, out, lse, scale=None, causal=True, window=
         grads.append(t)
     args, out, lse, dev = _attention_args(q, k, v, out, lse, dout, [t.data_ptr() for t in grads], scale, causal,
                                           window, softcap, slopes, documents, prefix, lengths, starts)
+    if any(t is not None for t in given):
+        # dq is written before q and dout are read for dk and dv, and while k and v are read for it
+        dq, dk, dv = given
+        reads = ((q, "q"), (dout, "dout"), (slopes, "slopes"), (documents, "documents"), (prefix, "prefix"),
+                 (lengths, "lengths"), (starts, "starts"))
+        if dq is not None:
+            _apart(dq, "dq", *reads, (k, "k"), (v, "v"), (out, "out", True), (lse, "lse"), (dk, "dk"), (dv, "dv"))
+        for t, name in ((dk, "dk"), (dv, "dv")):
+            if t is not None:
+                _apart(t, name, *reads, (k, "k", True), (v, "v", True))
+        if dk is not None:
+            _apart(dk, "dk", (dv, "dv"))
     ptr, size, ws = _ws(workspace, _lib.muon_attention_backward_workspace_size(args) or 256, dev)
     _call(dev, _lib.muon_attention_backward, args, ptr, size)
     return tuple(grads)
@@ -296,9 +393,17 @@ def qk_norm_rope(q, k, table, positions=None, q_weight=None, k_weight=None, eps=
     pair (i, i + d / 2); ``positions`` (batch, s) int32 (default 0 .. s - 1;
     one outside the table gives NaN); ``q_weight`` and ``k_weight`` (d,)
     float32 scale the norms (default ones).  d is even and up to 512; d a
-    multiple of 16 (float32: 8) with 16-byte aligned heads runs fastest."""
+    multiple of 16 (float32: 8) with 16-byte aligned heads runs fastest.
+    ``q_out`` may be q itself and ``k_out`` k; else they must not share memory
+    with anything."""
     args, results, dev = _qk_args(q, k, table, positions, q_weight, k_weight, eps, (q_out, k_out, "out of "), None,
                                   (None, None))
+    if q_out is not None or k_out is not None:
+        reads = ((table, "table"), (positions, "positions"), (q_weight, "q_weight"), (k_weight, "k_weight"))
+        if q_out is not None:
+            _apart(q_out, "q_out", (q, "q", True), (k, "k"), *reads, (k_out, "k_out"))
+        if k_out is not None:
+            _apart(k_out, "k_out", (q, "q"), (k, "k", True), *reads)
     _call(dev, _lib.muon_qk_norm_rope, args)
     return results[0], results[1]
 
@@ -350,6 +455,7 @@ def embedding(tokens, table, scale=1.0, dtype=None, out=None):
         if dtype is not None and dtype != out.dtype:
             raise TypeError(f"out is {out.dtype}, not {dtype}")
         _exactly(out, "out", out.dtype, dev, shape)
+        _apart(out, "out", (tokens, "tokens"), (table, "table"))
     _call(dev, _lib.muon_embedding, tokens.data_ptr(), token_bytes, table.data_ptr(), _DTYPE[table.dtype],
           out.data_ptr(), _DTYPE[out.dtype], tokens.numel(), table.shape[0], table.shape[1], float(scale))
     return out
@@ -379,6 +485,7 @@ def embedding_backward(dout, tokens, vocab, scale=1.0, dtype=None, out=None, wor
         if dtype is not None and dtype != out.dtype:
             raise TypeError(f"out is {out.dtype}, not {dtype}")
         _exactly(out, "out", out.dtype, dev, (vocab, width))
+        _apart(out, "out", (tokens, "tokens"), (dout, "dout"))
     ptr, size, ws = _ws(workspace, _lib.muon_embedding_backward_workspace_size(n, vocab, width) or 256, dev)
     _call(dev, _lib.muon_embedding_backward, tokens.data_ptr(), token_bytes, dout.data_ptr(), _DTYPE[dout.dtype],
           out.data_ptr(), _DTYPE[out.dtype], n, vocab, width, float(scale), ptr, size)
