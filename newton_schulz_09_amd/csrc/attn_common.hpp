@@ -663,10 +663,13 @@ __device__ __forceinline__ float score(const Score& s, float x, float dist) {
     return z;
 }
 
-// The extras of a call.
+// The extras of a call.  Without any, dK and dV start their products from -lse /
+// scale, which passes float32's range at scales near 2^-124: small ones go the
+// way of a bias of zero, which subtracts lse afterwards.
+constexpr float kMinPlainScale = 0x1p-100f;
 inline int score_extras(const AttnArgs& a) {
     if (a.softcap > kMaxPlainCap) return kCap | kBias | kWide;
-    return (a.softcap > 0.0f ? kCap : 0) | (a.slopes ? kBias : 0);
+    return (a.softcap > 0.0f ? kCap : 0) | (a.slopes || a.scale < kMinPlainScale ? kBias : 0);
 }
 
 }  // namespace attn

@@ -65,3 +65,13 @@ def test_small_caps(lm, cap):
     q, k, v, dout = make(1, 100, 100, 2, 1, 64)
     q[:, ::7] = 0
     check(lm, q, k, v, dout, softcap=cap)
+
+
+@pytest.mark.parametrize("scale,size", [(2e-38, 2e18), (1e-37, 1e18), (3e-33, 1e16), (2.0 ** -101, 1e15), (2.0 ** -99, 1e15),
+                                        (1e-6, 1e3), (1e6, 1e-3)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scales(lm, scale, size, d):
+    """Scores of ordinary size from a scale and heads that are not."""
+    q, k, v, dout = make(1, 140, 140, 2, 1, d, size=1.0)
+    check(lm, q * size, k * size, v, dout, scale=scale)
+    check(lm, q * size, k * size, v, dout, scale=scale, window=30, causal=False)
