@@ -139,7 +139,8 @@ int muon_qk_norm_rope_backward(const muon_qk_norm_rope_args *args, void *workspa
 
 /*
  * out[i] = scale table[tokens[i]] (float32, rounded once to out's type).  A
- * token outside 0 .. vocab - 1 gives a row of NaN.
+ * token outside 0 .. vocab - 1 gives a row of NaN.  n and vocab are below 2^31 -
+ * 1 and width up to 2^20 (MUON_ERR_UNSUPPORTED past that).
  *  tokens : [n], int64 (token_bytes 8) or int32 (token_bytes 4).
  *  table  : [vocab][width] of table_type; out: [n][width] of out_type.
  */

@@ -72,9 +72,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_dq(const AttnArgs) {
     __shared__ __align__(16) int sdocs[ST][kTile];
     const Args a = arguments();
     const int H = a->b * a->hq, U = a->b * a->hkv;
-    const int blk = blockIdx.x, e = blk % H;
+    const int blocks = (a->sq + BM - 1) / BM;
+    if (block_place() >= static_cast<uint32_t>(blocks) * H) return;
+    const int blk = block_place(), e = blk % H;
     const int u = e % U, b = u / a->hkv, kvh = u % a->hkv, h = kvh * a->grp + e / U;
-    const int i0 = ((gridDim.x / H) - 1 - blk / H) * BM;
+    const int i0 = (blocks - 1 - blk / H) * BM;
     const int i1 = i0 + BM < a->sq ? i0 + BM : a->sq;
     const Seq seq = sequence(a, b);
     const int w0 = i0 + wave_id() * 32, w1 = w0 + 32 < a->sq ? w0 + 32 : a->sq;
@@ -225,7 +227,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 || PAIR ? 2 : 1) void k_attn_dkv(
     __shared__ __align__(16) bf16x8 handed[PAIR ? NW : 1][PAIR ? 4 : 1][64];
     const Args a = arguments();
     const int U = a->b * a->hkv;
-    const int blk = blockIdx.x, u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
+    if (block_place() >= static_cast<uint32_t>((a->sk + BN - 1) / BN) * U) return;
+    const int blk = block_place(), u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
     const int j0 = blk / U * BN;
     const Seq seq = sequence(a, b);
     const int part = PAIR ? wave_id() & 1 : 0;
@@ -465,19 +468,19 @@ done:
 template <int DP, int MOD>
 void dq(const AttnArgs& a, hipStream_t stream) {
     constexpr int NW = 4, BM = 32 * NW;
-    const int blocks = (a.sq + BM - 1) / BM * a.b * a.hq;
-    k_attn_dq<DP, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    const int64_t blocks = static_cast<int64_t>((a.sq + BM - 1) / BM) * a.b * a.hq;
+    k_attn_dq<DP, NW, MOD><<<long_grid(blocks, 64 * NW), 64 * NW, 0, stream>>>(a);
 }
 template <int DP, int MOD>
 void dkv(const AttnArgs& a, hipStream_t stream) {
     constexpr int BN = 128;
-    const int blocks = (a.sk + BN - 1) / BN * a.b * a.hkv;
+    const int64_t blocks = static_cast<int64_t>((a.sk + BN - 1) / BN) * a.b * a.hkv;
     // pairs where the cap makes the vector work long enough to hide the
     // handing over: capped documents of 16384 tokens 258 -> 232 us, capped 2 x
     // 2048 tokens of 12 heads (both kernels) 160 -> 155; without a cap 16 x 1024
     // tokens of 6 heads 151 -> 159, 4 x 4096 of 16 heads over 4 945 -> 975
-    if constexpr (DP == 128 && (MOD & kCap) != 0) k_attn_dkv<DP, 8, true, MOD><<<blocks, 512, 0, stream>>>(a);
-    else k_attn_dkv<DP, 4, false, MOD><<<blocks, 256, 0, stream>>>(a);
+    if constexpr (DP == 128 && (MOD & kCap) != 0) k_attn_dkv<DP, 8, true, MOD><<<long_grid(blocks, 512), 512, 0, stream>>>(a);
+    else k_attn_dkv<DP, 4, false, MOD><<<long_grid(blocks, 256), 256, 0, stream>>>(a);
 }
 
 }  // namespace

@@ -125,9 +125,11 @@ __global__ __launch_bounds__(64 * NW, DP == 64 ? 3 : 2) void k_attn_fwd(const At
     const Args a = arguments();
     // heads that share keys run side by side; the longest tiles go first
     const int H = a->b * a->hq, U = a->b * a->hkv;
-    const int blk = blockIdx.x, e = blk % H;
+    const int blocks = (a->sq + BM - 1) / BM;
+    if (block_place() >= static_cast<uint32_t>(blocks) * H) return;
+    const int blk = block_place(), e = blk % H;
     const int u = e % U, b = u / a->hkv, kvh = u % a->hkv, h = kvh * a->grp + e / U;
-    const int i0 = ((gridDim.x / H) - 1 - blk / H) * BM;
+    const int i0 = (blocks - 1 - blk / H) * BM;
     const int i1 = i0 + BM < a->sq ? i0 + BM : a->sq;
     const Seq seq = sequence(a, b);
     const int w0 = i0 + wave_id() * 32, w1 = w0 + 32 < a->sq ? w0 + 32 : a->sq;
@@ -214,7 +216,8 @@ __global__ __launch_bounds__(64 * NW, 1) void k_attn_split(const AttnArgs) {
     __shared__ __align__(16) int sdocs[NW][kTile];
     __shared__ float sml[NW][2][32];
     const int U = a->b * a->hkv, rows = a->grp * a->sq;
-    const int blk = blockIdx.x, u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
+    if (block_place() >= static_cast<uint32_t>((rows + 31) / 32) * a->splits * U) return;
+    const int blk = block_place(), u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
     const int split = blk / U % a->splits, rt = blk / U / a->splits;
     const Seq seq = sequence(a, b);
     const int wave = wave_id(), lane = lane_id();
@@ -348,7 +351,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_attn_split(const AttnArgs) {
 __global__ __launch_bounds__(256) void k_attn_merge(const AttnArgs) {
     const Args a = arguments();
     const int lane = lane_id(), splits = a->splits, d = a->d;
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 4 + wave_id(), rows = static_cast<int64_t>(a->b) * a->hq * a->sq;
+    const int64_t at = static_cast<int64_t>(block_place()) * 4 + wave_id(), rows = static_cast<int64_t>(a->b) * a->hq * a->sq;
     if (at >= rows) return;
     const float* ml = a->part + 2 * at * splits;
     const float* o = a->part + 2 * rows * splits + at * splits * d;
@@ -398,9 +401,9 @@ __global__ __launch_bounds__(256) void k_attn_merge(const AttnArgs) {
 // (lowest, highest) document of each kTile tokens, one wave per tile.
 __global__ __launch_bounds__(256) void k_doc_tiles(const AttnArgs) {
     const Args a = arguments();
-    const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + wave_id();
+    const int64_t w = static_cast<int64_t>(block_place()) * 4 + wave_id();
+    if (w >= static_cast<int64_t>(a->b) * a->n_tiles) return;
     const int b = static_cast<int>(w / a->n_tiles), t = static_cast<int>(w % a->n_tiles);
-    if (b >= a->b) return;
     const int j = t * kTile + lane_id();
     int lo = 0x7fffffff, hi = static_cast<int>(0x80000000u);
     if (j < a->sk) lo = hi = a->documents[b * a->doc_b + j];
@@ -416,20 +419,20 @@ __global__ __launch_bounds__(256) void k_doc_tiles(const AttnArgs) {
 template <int DP, int MOD>
 void fwd(const AttnArgs& a, hipStream_t stream) {
     constexpr int NW = 4, BM = 32 * NW;
-    const int blocks = (a.sq + BM - 1) / BM * a.b * a.hq;
-    k_attn_fwd<DP, NW, MOD><<<blocks, 64 * NW, 0, stream>>>(a);
+    const int64_t blocks = static_cast<int64_t>((a.sq + BM - 1) / BM) * a.b * a.hq;
+    k_attn_fwd<DP, NW, MOD><<<long_grid(blocks, 64 * NW), 64 * NW, 0, stream>>>(a);
 }
 
 template <int DP, int MOD>
 void split(const AttnArgs& a, hipStream_t stream) {
-    const int blocks = (a.grp * a.sq + 31) / 32 * a.splits * a.b * a.hkv;
+    const int64_t blocks = static_cast<int64_t>((a.grp * a.sq + 31) / 32) * a.splits * a.b * a.hkv;
     // 8 waves fill a CU's LDS with tiles of 64; with more workgroups than CUs
     // two of 4 waves share it, one computing while the other starts or ends
-    if (DP == 64 && blocks <= 256) k_attn_split<DP, DP == 64 ? 8 : 4, MOD><<<blocks, 64 * (DP == 64 ? 8 : 4), 0, stream>>>(a);
-    else k_attn_split<DP, 4, MOD><<<blocks, 64 * 4, 0, stream>>>(a);
+    if (DP == 64 && blocks <= 256) k_attn_split<DP, DP == 64 ? 8 : 4, MOD><<<static_cast<int>(blocks), 64 * (DP == 64 ? 8 : 4), 0, stream>>>(a);
+    else k_attn_split<DP, 4, MOD><<<long_grid(blocks, 256), 256, 0, stream>>>(a);
     if (a.splits > 1) {
         const int64_t rows = static_cast<int64_t>(a.b) * a.hq * a.sq;
-        k_attn_merge<<<static_cast<int>((rows + 3) / 4), 256, 0, stream>>>(a);
+        k_attn_merge<<<long_grid((rows + 3) / 4, 256), 256, 0, stream>>>(a);
     }
 }
 
@@ -437,7 +440,7 @@ void split(const AttnArgs& a, hipStream_t stream) {
 
 hipError_t launch_attn_doc_tiles(const AttnArgs& a, hipStream_t stream) {
     const int64_t waves = static_cast<int64_t>(a.b) * a.n_tiles;
-    k_doc_tiles<<<static_cast<int>((waves + 3) / 4), 256, 0, stream>>>(a);
+    k_doc_tiles<<<long_grid((waves + 3) / 4, 256), 256, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -79,7 +79,7 @@ template <typename TS, typename TD, int V>
 __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a, int lanes) {
     const int l = threadIdx.x % lanes, per = 256 / lanes;
     const int pieces = a.width / V;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * per + threadIdx.x / lanes;
+    const int64_t i = static_cast<int64_t>(block_place()) * per + threadIdx.x / lanes;
     if (i >= a.n) return;
     const int64_t t = token_at(a, i);
     const bool known = t >= 0 && t < a.vocab;
@@ -117,7 +117,8 @@ __global__ __launch_bounds__(64 * kSortWaves) void k_embed_sort(const EmbedArgs 
     __shared__ int32_t below[kSortWaves];
     __shared__ int32_t wsum[kSortWaves];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t lo = static_cast<int64_t>(blockIdx.x) * span;
+    const int64_t lo = static_cast<int64_t>(block_place()) * span;
+    if (lo >= a.vocab) return;
     const uint32_t base32 = static_cast<uint32_t>(lo);  // vocab is below 2^31
     const uint32_t rows = static_cast<uint32_t>(lo + span <= a.vocab ? span : a.vocab - lo);
     for (int i = threadIdx.x; i < kSortWaves * kSortSpan; i += blockDim.x) (&cnt[0][0])[i] = 0;
@@ -236,8 +237,10 @@ __global__ __launch_bounds__(256) void k_embed_sum(const EmbedArgs a, int window
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.0f;
-    if (static_cast<int>(blockIdx.x) >= windows) {
-        const int64_t r0 = static_cast<int64_t>(blockIdx.x - windows) * kZeroRows;
+    const int64_t block = block_place();
+    if (block >= windows) {
+        const int64_t r0 = (block - windows) * kZeroRows;
+        if (r0 >= a.vocab) return;
         const int rows = a.vocab - r0 < kZeroRows ? static_cast<int>(a.vocab - r0) : kZeroRows;
         if (static_cast<int>(threadIdx.x) <= rows) s_off[threadIdx.x] = a.offset[r0 + threadIdx.x];
         __syncthreads();
@@ -246,7 +249,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const EmbedArgs a, int window
             if (s_off[r] == s_off[r + 1]) store_e<TD, V>(static_cast<TD*>(a.dst) + (r0 + r) * a.width + c, acc);
         return;
     }
-    const int64_t total = a.offset[a.vocab], w0 = static_cast<int64_t>(blockIdx.x) * a.window;
+    const int64_t total = a.offset[a.vocab], w0 = block * a.window;
     if (w0 >= total) return;
     const int n = total - w0 < a.window ? static_cast<int>(total - w0) : a.window;
     if (static_cast<int>(threadIdx.x) < n + 2) {
@@ -281,7 +284,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const EmbedArgs a, int window
                     if (crosses || !ends) {
                         // began before, or goes on after: a part (the first
                         // run's if it began before)
-                        float* p = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (crosses ? 0 : 1)) * a.width + c;
+                        float* p = a.part + (block * 2 + (crosses ? 0 : 1)) * a.width + c;
 #pragma unroll
                         for (int k = 0; k < V; ++k) p[k] = acc[k];
                     } else {
@@ -298,13 +301,13 @@ __global__ __launch_bounds__(256) void k_embed_sum(const EmbedArgs a, int window
     }
 }
 
-// The run that begins in window blockIdx.x and goes on after it: the sum of its
+// The run that begins in window block_place() and goes on after it: the sum of its
 // parts, every fourth by each wave, the waves' sums joined in their order.
 template <typename TD, int V>
 __global__ __launch_bounds__(256) void k_embed_join(const EmbedArgs a) {
     __shared__ float s[3][64][V];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t total = a.offset[a.vocab], w = blockIdx.x, next = (w + 1) * a.window;
+    const int64_t total = a.offset[a.vocab], w = block_place(), next = (w + 1) * a.window;
     if (next >= total) return;
     const int t = a.ids[next - 1];
     if (a.ids[next] != t) return;
@@ -355,7 +358,8 @@ __global__ __launch_bounds__(256) void k_embed_direct(const EmbedArgs a, int row
     __shared__ uint16_t sorted[kDirectTokens];
     __shared__ int32_t count[4], first[kDirectRows + 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows;
+    const int64_t r0 = static_cast<int64_t>(block_place()) * rows;
+    if (r0 >= a.vocab) return;
     const int mine = a.vocab - r0 < rows ? static_cast<int>(a.vocab - r0) : rows;
     const int n = static_cast<int>(a.n), part = (n + 3) / 4;
     const int i1 = (wave + 1) * part < n ? (wave + 1) * part : n;
@@ -424,7 +428,7 @@ int row_lanes(int pieces) {
 template <typename TS, typename TD, int V>
 void fwd(const EmbedArgs& a, hipStream_t stream) {
     const int lanes = row_lanes(a.width / V), per = 256 / lanes;
-    k_embed<TS, TD, V><<<static_cast<uint32_t>((a.n + per - 1) / per), 256, 0, stream>>>(a, lanes);
+    k_embed<TS, TD, V><<<long_grid((a.n + per - 1) / per, 256), 256, 0, stream>>>(a, lanes);
 }
 
 template <typename TS, typename TD, int V>
@@ -438,25 +442,23 @@ void bwd(const EmbedArgs& a, hipStream_t stream) {
         rows = rows < 1 ? 1 : (rows < kDirectRows ? rows : kDirectRows);
         int lanes = 1;
         while (lanes < 256 && lanes < pieces) lanes <<= 1;
-        k_embed_direct<TS, TD, W><<<dim3(static_cast<uint32_t>((a.vocab + rows - 1) / rows),
-                                         static_cast<uint32_t>((pieces + lanes - 1) / lanes)),
-                                    256, 0, stream>>>(a, static_cast<int>(rows), lanes);
+        k_embed_direct<TS, TD, W><<<long_grid((a.vocab + rows - 1) / rows, 256, (pieces + lanes - 1) / lanes), 256, 0, stream>>>(
+            a, static_cast<int>(rows), lanes);
         return;
     }
     // 256 workgroups, one per CU, unless the table needs more
     int64_t span = (a.vocab + 255) / 256;
     if (span > kSortSpan) span = kSortSpan;
-    const uint32_t sorts = static_cast<uint32_t>((a.vocab + span - 1) / span);
+    const dim3 sorts = long_grid((a.vocab + span - 1) / span, 64 * kSortWaves);
     if (a.tokens64) k_embed_sort<true><<<sorts, 64 * kSortWaves, 0, stream>>>(a, static_cast<int>(span));
     else k_embed_sort<false><<<sorts, 64 * kSortWaves, 0, stream>>>(a, static_cast<int>(span));
     int threads = (pieces + 63) / 64 * 64;
     if (threads > 256) threads = 256;
     const int64_t windows = (a.n + a.window - 1) / a.window, zeros = (a.vocab + kZeroRows - 1) / kZeroRows;
-    k_embed_sum<TS, TD, W><<<dim3(static_cast<uint32_t>(windows + zeros), static_cast<uint32_t>((pieces + threads - 1) / threads)),
-                             threads, 0, stream>>>(a, static_cast<int>(windows));
+    k_embed_sum<TS, TD, W><<<long_grid(windows + zeros, threads, (pieces + threads - 1) / threads), threads, 0, stream>>>(
+        a, static_cast<int>(windows));
     if (windows > 1)
-        k_embed_join<TD, J><<<dim3(static_cast<uint32_t>(windows - 1), static_cast<uint32_t>((a.width / J + 63) / 64)), 256, 0,
-                              stream>>>(a);
+        k_embed_join<TD, J><<<long_grid(windows - 1, 256, (a.width / J + 63) / 64), 256, 0, stream>>>(a);
 }
 
 // fn<source, target, values a piece>

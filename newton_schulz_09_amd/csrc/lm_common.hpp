@@ -10,6 +10,15 @@
 
 namespace muon {
 
+// A launch of `blocks` workgroups (below 2^31): HIP takes fewer than 2^32 threads
+// along x, so longer grids go on along z.  A kernel finds its place with
+// block_place(), which may be past the last one.
+inline dim3 long_grid(int64_t blocks, int threads, int64_t y = 1) {
+    const int64_t most = ((int64_t{1} << 32) - 1) / threads, z = (blocks + most - 1) / most;
+    return dim3(static_cast<uint32_t>((blocks + z - 1) / z), static_cast<uint32_t>(y), static_cast<uint32_t>(z));
+}
+__device__ __forceinline__ uint32_t block_place() { return blockIdx.z * gridDim.x + blockIdx.x; }
+
 // Keys per LDS tile of every attention kernel, and tokens per entry of the
 // document-range table.
 constexpr int kTile = 64;

@@ -75,3 +75,59 @@ def test_scales(lm, scale, size, d):
     q, k, v, dout = make(1, 140, 140, 2, 1, d, size=1.0)
     check(lm, q * size, k * size, v, dout, scale=scale)
     check(lm, q * size, k * size, v, dout, scale=scale, window=30, causal=False)
+
+
+def test_more_workgroups_than_one_grid_dimension_takes(lm):
+    """2^24 workgroups of 256 threads: one key, so out = v, dv = dout, dq = dk = 0."""
+    b, d = 2 ** 24 + 3, 8
+    q, k, v, dout = (torch.randn(b, 1, 1, d, device="cuda").bfloat16() for _ in range(4))
+    print(f"attention of {b} sequences of one token", flush=True)
+    documents = torch.arange(b, dtype=torch.int32, device="cuda")[:, None]
+    out, lse = lm.attention(q, k, v, documents=documents)
+    assert torch.equal(out, v)
+    # the score itself: 8 products and the factor in float32, and the logarithm back
+    z = (q.double() * k.double()).sum(-1) / d ** 0.5
+    room = 32 * 2.0 ** -24 * ((q.double() * k.double()).abs().sum(-1) + 1)
+    assert bool(((lse.double().view(b, 1, 1) - z).abs() <= room).all())
+    dq, dk, dv = lm.attention_backward(dout, q, k, v, out, lse, documents=documents)
+    # P is 1 but for the exponent's rounding, 2^-20 at most; dP - delta the same of sum |dout v|
+    mag = 2.0 ** -18 * (dout.double() * v.double()).abs().sum(-1, keepdim=True)
+    assert bool(((dv - dout).abs().double() <= 2.0 ** -7 * dout.abs().double()).all())
+    assert bool((dq.abs().double() <= mag * k.double().abs()).all()) and bool((dk.abs().double() <= mag * q.double().abs()).all())
+
+
+def test_more_queries_than_one_grid_dimension_takes(lm):
+    """33 queries a sequence, so whole blocks and not the split over keys."""
+    b, s, d = 2 ** 24 + 1, 33, 8
+    print(f"attention of {b} sequences of {s} tokens", flush=True)
+    v = torch.randn(b, 1, 1, d, device="cuda").bfloat16()
+    q = torch.randn(1, 1, 1, d, device="cuda").bfloat16().expand(b, s, 1, d)
+    out, lse = lm.attention(q, v, v, causal=False)
+    assert torch.equal(out, v.expand(b, s, 1, d))
+    assert bool(torch.isfinite(lse).all())
+
+
+def test_more_rows_than_one_grid_dimension_takes(lm):
+    n, width = 2 ** 26 + 5, 65
+    print(f"embedding of {n} tokens", flush=True)
+    table = torch.randn(300, width, device="cuda").bfloat16()
+    tokens = torch.randint(0, 300, (n,), dtype=torch.int32, device="cuda")
+    out = lm.embedding(tokens, table)
+    for at in range(0, n, 2 ** 23):
+        assert torch.equal(out[at:at + 2 ** 23], table[tokens[at:at + 2 ** 23].long()]), at
+
+
+@pytest.mark.parametrize("n,vocab", [(700, 2 ** 29 + 77), (3000, 2 ** 31 - 2)])
+def test_larger_tables_than_one_grid_dimension_takes(lm, n, vocab):
+    """Gradients of tables of one column: one launch, and sort, sums and zeros."""
+    print(f"gradient of {n} tokens, {vocab} rows", flush=True)
+    g = torch.Generator().manual_seed(1)
+    rows = torch.tensor([0, 1, vocab // 2, vocab - 33, vocab - 2, vocab - 1])
+    tokens = rows[torch.randint(0, 6, (n,), generator=g)]
+    dout = torch.randint(-3, 4, (n, 1), generator=g).bfloat16()  # sums of whole numbers are exact
+    grad = torch.full((vocab, 1), 7.0, dtype=torch.bfloat16, device="cuda")
+    lm.embedding_backward(dout.cuda(), tokens.cuda(), vocab, out=grad)
+    want = torch.stack([dout[tokens == r].float().sum().bfloat16() for r in rows])
+    assert torch.equal(grad[rows.cuda()][:, 0].cpu(), want)
+    grad[rows.cuda()] = 0
+    assert not any(bool(x.any()) for x in grad.split(2 ** 28))
