@@ -334,7 +334,7 @@ __global__ __launch_bounds__(64 * NW, 1) void k_attn_split(const AttnArgs) {
         a->part[2 * p] = m;
         a->part[2 * p + 1] = empty ? 0.0f : sum;
     }
-    float* o = a->part + 2 * n + p * a->d;
+    float* o = a->part + part_outputs(n) + p * a->d;
 #pragma unroll
     for (int dt = 0; dt < DP / 32; ++dt)
 #pragma unroll
@@ -354,7 +354,7 @@ __global__ __launch_bounds__(256) void k_attn_merge(const AttnArgs) {
     const int64_t at = static_cast<int64_t>(block_place()) * 4 + wave_id(), rows = static_cast<int64_t>(a->b) * a->hq * a->sq;
     if (at >= rows) return;
     const float* ml = a->part + 2 * at * splits;
-    const float* o = a->part + 2 * rows * splits + at * splits * d;
+    const float* o = a->part + part_outputs(rows * splits) + at * splits * d;
     float m = neg_inf(), l = 0.0f;
     for (int s = lane; s < splits; s += 64) m = fmaxf(m, ml[2 * s + 1] != 0.0f ? ml[2 * s] : neg_inf());
 #pragma unroll

@@ -109,8 +109,10 @@ AttnPlan plan_forward(const muon_attention_args* x) {
     p.off_docs = at;
     if (x->documents) at = align256(at + static_cast<size_t>(x->batch) * tiles * sizeof(int2));
     p.off_part = at;
-    if (p.splits > 1)
-        at = align256(at + static_cast<size_t>(x->batch) * x->heads * x->sq * p.splits * (x->d + 2) * sizeof(float));
+    if (p.splits > 1) {
+        const int64_t n = x->batch * x->heads * x->sq * p.splits;
+        at = align256(at + static_cast<size_t>(part_outputs(n) + n * x->d) * sizeof(float));
+    }
     p.bytes = at > 256 ? at : 256;
     return p;
 }

@@ -45,6 +45,10 @@ struct AttnArgs {
     float scale, softcap;
 };
 
+// The partial results of n (row, chunk) pairs: 2 n floats of maxima and sums,
+// then d floats of output each from here on, aligned to their 16-byte stores.
+__host__ __device__ inline int64_t part_outputs(int64_t n) { return (2 * n + 3) / 4 * 4; }
+
 hipError_t launch_attn_doc_tiles(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_fwd(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_split(const AttnArgs& a, hipStream_t stream);

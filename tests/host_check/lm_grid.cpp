@@ -1,5 +1,6 @@
-// The grids of the language-model kernels (lm_common.hpp, long_grid): within
-// HIP's limits, and no workgroup missing, for up to 2^31 - 1 workgroups.
+// Host functions of lm_common.hpp.  Grids (long_grid): within HIP's limits, and
+// no workgroup missing, for up to 2^31 - 1 workgroups.  Partial outputs
+// (part_outputs): past the maxima and sums, and aligned to 16-byte stores.
 #include <stdio.h>
 #include <stdlib.h>
 
@@ -21,6 +22,11 @@ int main() {
                 }
                 ++checked;
             }
+    for (int64_t n = 1; n < 100000; ++n)
+        if (muon::part_outputs(n) < 2 * n || muon::part_outputs(n) > 2 * n + 3 || muon::part_outputs(n) % 4 != 0) {
+            fprintf(stderr, "outputs of %lld pairs at %lld\n", (long long)n, (long long)muon::part_outputs(n));
+            return 1;
+        }
     printf("grids ok: %ld\n", checked);
     return 0;
 }

@@ -131,3 +131,10 @@ def test_larger_tables_than_one_grid_dimension_takes(lm, n, vocab):
     assert torch.equal(grad[rows.cuda()][:, 0].cpu(), want)
     grad[rows.cuda()] = 0
     assert not any(bool(x.any()) for x in grad.split(2 ** 28))
+
+
+@pytest.mark.parametrize("heads,d", [(25, 64), (3, 80), (5, 128)])
+def test_odd_numbers_of_partial_results(lm, heads, d):
+    """One token over 3200 keys in 3 chunks: an odd number of (row, chunk) pairs
+    lies before the partial outputs."""
+    check(lm, *make(1, 1, 3200, heads, heads, d))

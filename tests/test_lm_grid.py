@@ -1,4 +1,5 @@
-"""The grids of the language-model kernels, on the CPU (tests/host_check/lm_grid.cpp)."""
+"""The grids of the language-model kernels and where their partial outputs lie,
+on the CPU (tests/host_check/lm_grid.cpp)."""
 
 import os
 import re
