@@ -53,9 +53,12 @@ extern "C" {
  * gradients.  Query head h uses key head h / (heads / kv_heads), and the
  * gradients of a shared key head sum over its query heads.
  *
- * Memory past lengths[batch] may hold anything, NaN included.  (A NaN or an
- * infinity at a key that some query of a batch sees can reach other queries
- * of the batch through 0 * inf.)
+ * Memory past lengths[batch] may hold anything, NaN included, and so may k and
+ * v past the last key that any query of the batch sees (a cache past its last
+ * position), and q and dout of a query that sees no key.  (Other NaNs and
+ * infinities can reach other rows of the batch through 0 * inf: also of keys in
+ * front of every window or of documents that no query has, and with both
+ * prefix and documents of queries past the last key's window.)
  *
  * Scores, statistics and sums are float32.  exp(z - lse) and the gradient of
  * the scores are rounded to bfloat16 as operands of the matrix cores; the

@@ -230,7 +230,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 || PAIR ? 2 : 1) void k_attn_dkv(
     if (block_place() >= static_cast<uint32_t>((a->sk + BN - 1) / BN) * U) return;
     const int blk = block_place(), u = blk % U, b = u / a->hkv, kvh = u % a->hkv;
     const int j0 = blk / U * BN;
-    const Seq seq = sequence(a, b);
+    Seq seq = sequence(a, b);
+    const int lead = only_queries_that_see(seq, a);
     const int part = PAIR ? wave_id() & 1 : 0;
     const int w0 = j0 + (PAIR ? wave_id() >> 1 : wave_id()) * 32;
     auto key_span = [&](int lo, int hi) {
@@ -255,9 +256,9 @@ __global__ __launch_bounds__(64 * NW, DP == 64 || PAIR ? 2 : 1) void k_attn_dkv(
     in_vectors(g);
     in_vectors(w);
     Direct<DP, NT> lq, ld;
-    lq.init(a->q + b * a->q_b + static_cast<int64_t>(kvh) * a->grp * a->q_h, a->q_s, it.rows, a->d);
-    ld.init(a->dout + b * a->do_b + static_cast<int64_t>(kvh) * a->grp * a->do_h, a->do_s, it.rows, a->d);
-    const float* stat = a->stats + (static_cast<int64_t>(b) * a->hq + kvh * a->grp) * a->sq;
+    lq.init(a->q + b * a->q_b + static_cast<int64_t>(kvh) * a->grp * a->q_h + lead * a->q_s, a->q_s, it.rows, a->d);
+    ld.init(a->dout + b * a->do_b + static_cast<int64_t>(kvh) * a->grp * a->do_h + lead * a->do_s, a->do_s, it.rows, a->d);
+    const float* stat = a->stats + (static_cast<int64_t>(b) * a->hq + kvh * a->grp) * a->sq + lead;
     const uint32_t at = lds_addr(lds);
     int tile[ST], mode[ST], left = a->grp - 1;  // heads after the tiles' own
     Score sc[ST], head = score_of<MOD>(a, kvh * a->grp);

@@ -348,8 +348,9 @@ __device__ __forceinline__ void store_rows(const f32x16 (&o)[DP / 32], float mul
 
 // What one sequence of the batch sees.
 struct Seq {
-    int n;      // keys (and positions) below this one are real
+    int n;      // keys (and positions) below this one are real, and within reach of a query
     int start;  // position of query 0
+    int sq;     // queries from there on
     int pre;    // keys below this one are seen by every query
     int b;
     const int32_t* doc;
@@ -365,13 +366,36 @@ __device__ __forceinline__ Seq sequence(Args a, int b) {
     int st = a->sk - a->sq;
     if (a->starts) st = a->starts[b];
     s.start = st < -kMaxPos ? -kMaxPos : (st > kMaxPos ? kMaxPos : st);
+    s.sq = a->sq;
     s.pre = 0;
     if (a->prefix) {
         const int p = a->prefix[b];
         s.pre = p < 0 ? 0 : (p < s.n ? p : s.n);
     }
     s.doc = a->documents ? a->documents + static_cast<int64_t>(b) * a->doc_b : nullptr;
+    // keys past the last query's reach are not read (0 times what lies there
+    // need not be 0: a cache may hold anything past its last position)
+    if (a->causal || a->window) {
+        int end = s.start + s.sq;
+        if (!a->causal) end += a->window - 1;
+        if (end < s.pre) end = s.pre;
+        if (end < s.n) s.n = end;
+    }
     return s;
+}
+// Leaves out the queries before the first and past the last that see any key
+// (dK and dV, which read every query's rows, must not read theirs); returns how
+// many were left out in front.  With a prefix every query sees keys, but for
+// those past the last key's window if the prefix holds other documents only.
+__device__ __forceinline__ int only_queries_that_see(Seq& s, Args a) {
+    if (s.pre > 0 || (!a->causal && !a->window)) return 0;
+    int lead = (a->causal ? 0 : 1 - a->window) - s.start;
+    if (a->window && s.n + a->window - 1 - s.start < s.sq) s.sq = s.n + a->window - 1 - s.start;
+    if (lead > s.sq) lead = s.sq;
+    if (lead < 0) lead = 0;
+    s.start += lead;
+    s.sq -= lead;
+    return lead;
 }
 __device__ __forceinline__ int doc_of(const Seq& s, Args a, int pos) {
     const int p = pos < 0 ? 0 : (pos < a->sk ? pos : a->sk - 1);
@@ -547,7 +571,7 @@ __device__ __forceinline__ Col col_of(const Seq& s, Args a, int j) {
     Col r;
     r.pos = j;
     r.lo = s.start;
-    r.hi = s.start + a->sq - 1;
+    r.hi = s.start + s.sq - 1;
     if (a->lengths && r.hi >= s.n) r.hi = s.n - 1;
     if (j >= s.pre) {
         if (a->causal && j > r.lo) r.lo = j;
@@ -586,7 +610,7 @@ struct QueryTiles {
     }
     // rows: queries that are real
     __device__ __forceinline__ void init(const Seq& s, Args a, const Span& g, const Span& w) {
-        rows = a->sq;
+        rows = s.sq;
         if (a->lengths && s.n - s.start < rows) rows = s.n - s.start;
         int lo = 0, hi = rows - 1;
         if (g.p0 >= s.pre) {

@@ -271,7 +271,9 @@ def attention(q, k, v, scale=None, causal=True, window=0, softcap=0.0, slopes=No
     ``out`` may be q itself; else given outputs must not share memory with
     anything (nor may elements of ``out`` among themselves).
 
-    A query that sees no key gets out = 0 and lse = -inf.  A step of generation
+    A query that sees no key gets out = 0 and lse = -inf.  Keys and values past
+    the last one that any query of the batch sees may hold anything, as the
+    rest of a cache does.  A step of generation
     (up to 32 query rows per key head) reads each cached key and value once."""
     given = out, lse
     args, out, lse, dev = _attention_args(q, k, v, out, lse, None, (0, 0, 0), scale, causal, window, softcap, slopes,
