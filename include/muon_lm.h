@@ -97,7 +97,8 @@ size_t muon_attention_backward_workspace_size(const muon_attention_args *args);
 /*
  * out and lse from q, k and v.  out may be q (the same pointer and strides).
  * Errors: MUON_ERR_INVALID_ARG (null pointers, negative sizes, heads not a
- * multiple of kv_heads, misaligned pointers or strides, a scale that is not
+ * multiple of kv_heads, misaligned pointers (16 bytes; 4 for lse, slopes and
+ * the masks) or strides, a negative documents_stride, a scale that is not
  * positive and finite, a negative softcap or window), MUON_ERR_UNSUPPORTED (d
  * not a multiple of 8 up to 128, sq or sk of 2^29 or more, row strides of
  * 2^24 elements or more, more than 2^31 - 1 workgroups), MUON_ERR_WORKSPACE.

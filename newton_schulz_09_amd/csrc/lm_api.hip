@@ -80,6 +80,16 @@ int check_rows(const char* name, const void* p, const int64_t* strides, int64_t 
     return MUON_OK;
 }
 
+int check_masks(const muon_attention_args* x) {
+    for (const void* p : {static_cast<const void*>(x->slopes), static_cast<const void*>(x->documents),
+                          static_cast<const void*>(x->prefix), static_cast<const void*>(x->lengths),
+                          static_cast<const void*>(x->starts)})
+        if (!aligned(p, 4)) return refuse(MUON_ERR_INVALID_ARG, "slopes or a mask is not aligned to 4 bytes");
+    if (x->documents && x->batch > 1 && x->documents_stride < 0)
+        return refuse(MUON_ERR_INVALID_ARG, "documents: stride %lld is negative", (long long)x->documents_stride);
+    return MUON_OK;
+}
+
 struct AttnPlan {
     bool split;
     int splits, chunk;
@@ -255,6 +265,11 @@ int run_qk(const muon_qk_norm_rope_args* x, bool backward, void* ws, size_t ws_b
                 }
         }
     }
+    for (const void* p : {static_cast<const void*>(x->weight[0]), static_cast<const void*>(x->weight[1]),
+                          static_cast<const void*>(backward ? x->dweight[0] : nullptr),
+                          static_cast<const void*>(backward ? x->dweight[1] : nullptr),
+                          static_cast<const void*>(x->table), static_cast<const void*>(x->positions)})
+        if (!aligned(p, 4)) return refuse(MUON_ERR_INVALID_ARG, "a weight, the table or positions are not aligned to 4 bytes");
     const bool any = rows && (x->heads[0] > 0 || x->heads[1] > 0);
     if (any && !x->table) return refuse(MUON_ERR_INVALID_ARG, "table is null");
     const bool want_dw = backward && (x->dweight[0] || x->dweight[1]);
@@ -378,6 +393,7 @@ size_t muon_attention_backward_workspace_size(const muon_attention_args* args) {
 int muon_attention(const muon_attention_args* x, void* ws, size_t ws_bytes, void* stream) {
     using namespace muon;
     if (int st = check_sizes(x)) return st;
+    if (int st = check_masks(x)) return st;
     if (int st = check_rows("q", x->q, x->q_strides, x->batch, x->sq, x->heads)) return st;
     if (int st = check_rows("k", x->k, x->k_strides, x->batch, x->sk, x->kv_heads)) return st;
     if (int st = check_rows("v", x->v, x->v_strides, x->batch, x->sk, x->kv_heads)) return st;
@@ -398,6 +414,7 @@ int muon_attention(const muon_attention_args* x, void* ws, size_t ws_bytes, void
 int muon_attention_backward(const muon_attention_args* x, void* ws, size_t ws_bytes, void* stream) {
     using namespace muon;
     if (int st = check_sizes(x)) return st;
+    if (int st = check_masks(x)) return st;
     if (int st = check_rows("q", x->q, x->q_strides, x->batch, x->sq, x->heads)) return st;
     if (int st = check_rows("k", x->k, x->k_strides, x->batch, x->sk, x->kv_heads)) return st;
     if (int st = check_rows("v", x->v, x->v_strides, x->batch, x->sk, x->kv_heads)) return st;
