@@ -301,7 +301,8 @@ __global__ __launch_bounds__(64 * NW, DP == 64 || PAIR ? 2 : 1) void k_attn_dkv(
     settle(vf);
 
     constexpr int KT = DP / 16, DT = DP / 32, kAhead = DP == 64 ? 3 : 8;
-    auto step = [&](uint32_t tq, uint32_t td, const float* sl, const float* sdel, const int* sdoc, bool masked, const Score& score, int q0) {
+    // (with a parameter of a template, so that it exists only where it is called)
+    auto step = [&](auto, uint32_t tq, uint32_t td, const float* sl, const float* sdel, const int* sdoc, bool masked, const Score& score, int q0) {
         const int h4 = 4 * (lane_id() >> 5);
         f32x16 s[2], dp[2];
         bf16x8 pp[2][2], pd[2][2], ring[kAhead];
@@ -372,7 +373,7 @@ __global__ __launch_bounds__(64 * NW, DP == 64 || PAIR ? 2 : 1) void k_attn_dkv(
             in_order();
         });
     };
-    auto share = [&](uint32_t tq, uint32_t td, const float* sl, const float* sdel, const int* sdoc, int seen, const Score& score, int q0) {
+    auto share = [&](auto, uint32_t tq, uint32_t td, const float* sl, const float* sdel, const int* sdoc, int seen, const Score& score, int q0) {
         // this wave's block is `part`
         const int h4 = 4 * (lane_id() >> 5), r0 = 32 * part + h4;
         constexpr int kRing = 4;
@@ -451,10 +452,10 @@ __global__ __launch_bounds__(64 * NW, DP == 64 || PAIR ? 2 : 1) void k_attn_dkv(
             landed();
             fetch(1 - x);
             if constexpr (PAIR)
-                share(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x], sc[x],
+                share(0, at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x], sc[x],
                       tile[x] * kTile);
             else if (mode[x] != 0)
-                step(at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x] == 1 || !whole, sc[x],
+                step(0, at + 2 * x * TB, at + (2 * x + 1) * TB, sstat[x][0], sstat[x][1], seq.doc ? sdocs[x] : nullptr, mode[x] == 1 || !whole, sc[x],
                      tile[x] * kTile);
         }
     }
