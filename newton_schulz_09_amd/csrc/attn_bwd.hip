@@ -4,11 +4,14 @@
 // block of keys.  P is made again from the scores and lse; recomputing the
 // two products S and dO V^T costs 7 products instead of 5.
 //
-// 16 x 1024 tokens of 12 heads of 64, causal: dQ 61 us, dK and dV 72, both bound
-// by vector work (an exponential and 4 other instructions a score) and its
-// waits.  One packed sequence of 16384 tokens, 6 heads of 128, capped scores,
-// window 4096, documents: 190 and 224 us.  delta = sum dO O is taken from the
-// bf16 O that the caller holds.
+// 16 x 1024 tokens of 12 heads of 64, causal: dQ 61 us, dK and dV 72.  By counters
+// no pipe bounds them: of the cycles in which a CU holds waves (over 90 % of the
+// kernel) the vector pipe is busy for 44 and 40 %, the matrix pipe for 34 and 38 %,
+// LDS for 17 and 28 %; the rest are waits of two waves a SIMD for each other's
+// steps.  One packed sequence of 16384 tokens, 6 heads of 128, capped scores,
+// window 4096, documents: 190 and 224 us, vector 55 and 42 %, matrix 39 and 30 %,
+// and CUs hold waves for 55 and 76 % of the kernel (blocks of unequal work).
+// delta = sum dO O is taken from the bf16 O that the caller holds.
 #include "attn_common.hpp"
 
 namespace muon {

@@ -4,11 +4,18 @@
 // Scores are made transposed (keys x queries), so a lane holds scores of one
 // query only: maximum and sum take one exchange between the halves of the
 // wave, and the probabilities are the next product's operand as they lie.
-// Heads of 64 are bound by vector work (4.4 instructions a score, one of them
-// a quarter-rate exponential: 16 x 1024 tokens of 12 heads, causal, 43 us, 600
-// TFLOP/s of visible pairs); heads of 128 by both pipes (4 x 4001 tokens, 32
-// heads over 8, prefix: 549 to 600 us, 910 to 1000 TFLOP/s, where a library
-// product of 8192^3 reaches 1200).
+// By counters, of the cycles in which a CU holds waves: heads of 64 (16 x 1024
+// tokens of 12 heads, causal: 43 us, 600 TFLOP/s of visible pairs) have the vector
+// pipe busy for 67 % (4.4 instructions a score) and the matrix pipe for 33 %, one
+// after the other rather than side by side: the scores' products have no vector
+// work under them, nor the maximum and the first half of the exponentials any
+// products.  Heads of 128 (4 x 4001 tokens, 32 heads over 8, prefix: 549 to 600 us,
+// 910 to 1000 TFLOP/s, where a library product of 8192^3 reaches 1200): 51 % and
+// 55 %.  LDS reads take 17 to 33 % and 28 to 55 % (a wave reads a whole tile for 32
+// queries; the counter's busy cycles, and 128 bytes a clock).  Packed documents of
+// 16384 tokens, cap, 6 heads of 128 (162 us): 59 % and 30 %, but CUs hold waves for
+// half of the kernel only: 768 workgroups whose work depends on the place in the
+// document, dealt by position.
 #include "attn_common.hpp"
 
 namespace muon {

@@ -1,6 +1,7 @@
 // Embedding: out[i] = scale * table[token[i]], and the table's gradient
 // dtable[v] = scale * sum of dout[i] over the i with token[i] = v, summed in
-// the order of i in float32, without atomics on floating values.
+// float32 in one fixed order (that of i within a window, windows by fours),
+// without atomics on floating values.
 //
 // Both are bound by memory.  The gradient sorts the tokens first (k_embed_sort,
 // stable), then sums windows of sorted entries and writes the rows of tokens
@@ -8,8 +9,8 @@
 // workgroups however often it occurs, and last joins the runs that cross
 // windows (k_embed_join).  Few tokens take one launch (k_embed_direct).
 //
-// 65536 tokens, 50304 x 768 float32 rows: forward 29 us (5 TB/s); gradient 71:
-// sort 19, sums and zeros 39 (255 MB), joins 9.
+// 65536 tokens, 50304 x 768 float32 rows: forward 29 us (5 TB/s); gradient 66 to
+// 78: sort 19, sums and zeros 39 (255 MB), joins 9.
 #include "../../include/muon.h"
 #include "lm_common.hpp"
 

@@ -1,5 +1,5 @@
-// Shared definitions of the language-model operators (muon_lm.h): launch
-// arguments, the visibility rules of attention, and the LDS tile layouts.
+// Shared definitions of the language-model operators (muon_lm.h): grids and
+// launch arguments.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -24,8 +24,7 @@ __device__ __forceinline__ uint32_t block_place() { return blockIdx.z * gridDim.
 constexpr int kTile = 64;
 
 // Arguments of every attention kernel, passed by value.  Strides are in
-// elements; the last dimension is contiguous.  Tensors the kernels write are
-// contiguous.
+// elements; the last dimension is contiguous.  lse, dq, dk and dv are contiguous.
 struct AttnArgs {
     const bf16_t *q, *k, *v, *dout;
     bf16_t *out, *dq, *dk, *dv;

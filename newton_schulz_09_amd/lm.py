@@ -8,6 +8,10 @@ not synchronise.  Tensors the library writes are new unless given.  The
 workspace comes from torch's allocator for the call unless given (it then is
 the caller's to keep apart between streams), so calls can be captured into a
 graph.  Same inputs give the same bits every time.
+
+As in ``muon``, nothing here is recorded by autograd: results carry no history,
+also where an argument requires a gradient.  ``lm_example`` shows the
+``autograd.Function`` around each pair of calls.
 """
 
 import ctypes
@@ -47,7 +51,6 @@ QK_NORM_MAX_D = 512
 
 _F32, _BF16 = torch.float32, torch.bfloat16
 _DTYPE = {_F32: muon.MUON_F32, _BF16: muon.MUON_BF16}
-_SIZE = {_F32: 4, _BF16: 2}
 # muon_attention_args and muon_qk_norm_rope_args: 8-byte fields throughout
 _ATTN = struct.Struct("9Q15q2Qq3Q8q2d")
 _QK = struct.Struct("10Q12q2qQqQ3qqd")
@@ -466,7 +469,7 @@ def embedding(tokens, table, scale=1.0, dtype=None, out=None):
 def embedding_backward(dout, tokens, vocab, scale=1.0, dtype=None, out=None, workspace=None):
     """Gradient (vocab, width) of ``embedding``'s table from ``dout`` (of
     tokens.shape + (width,), float32 or bfloat16, contiguous): for each row the
-    sum of its tokens' gradients times ``scale``, in float32 and in the tokens'
+    sum of its tokens' gradients times ``scale``, in float32 and in one fixed
     order, rounded once to ``dtype`` (default dout's).  Rows of tokens that do
     not occur are zero."""
     dev, token_bytes = _tokens(tokens)
