@@ -85,7 +85,7 @@ typedef struct muon_attention_args {
     const int32_t *starts;    /* [batch], or NULL: sk - sq; clamped to +-2^29 */
     int64_t batch, sq, sk, heads, kv_heads, d;
     int64_t causal;           /* 0 or 1 */
-    int64_t window;           /* 0: none */
+    int64_t window;           /* 0, or 2^29 and more: none */
     double scale;             /* > 0 */
     double softcap;           /* 0: none */
 } muon_attention_args;

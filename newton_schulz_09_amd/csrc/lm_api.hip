@@ -181,7 +181,7 @@ AttnArgs attn_args(const muon_attention_args* x, const AttnPlan& p, void* ws) {
     a.grp = a.hq / a.hkv;
     a.d = static_cast<int>(x->d);
     a.causal = x->causal != 0;
-    a.window = static_cast<int>(x->window < kMaxSeq ? x->window : kMaxSeq);
+    a.window = static_cast<int>(x->window < kMaxSeq ? x->window : 0);
     a.n_tiles = static_cast<int>(div_up(x->sk, kTile));
     a.splits = p.splits;
     a.chunk = p.chunk;

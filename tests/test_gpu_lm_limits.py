@@ -138,3 +138,16 @@ def test_odd_numbers_of_partial_results(lm, heads, d):
     """One token over 3200 keys in 3 chunks: an odd number of (row, chunk) pairs
     lies before the partial outputs."""
     check(lm, *make(1, 1, 3200, heads, heads, d))
+
+
+@pytest.mark.parametrize("window", [2 ** 29, 2 ** 40, 2 ** 62])
+@pytest.mark.parametrize("causal", [True, False])
+def test_windows_past_every_distance(lm, window, causal):
+    """The same bits as without a window, also for positions far from the keys."""
+    q, k, v, dout = make(3, 70, 200, 4, 2, 64)
+    starts = torch.tensor([2 ** 31 - 1, -2 ** 31, 100], dtype=torch.int32).cuda()
+    want = lm.attention(q, k, v, causal=causal, starts=starts)
+    got = lm.attention(q, k, v, causal=causal, starts=starts, window=window)
+    a = lm.attention_backward(dout, q, k, v, *want, causal=causal, starts=starts)
+    b = lm.attention_backward(dout, q, k, v, *got, causal=causal, starts=starts, window=window)
+    assert all(torch.equal(x, y) for x, y in zip((*want, *a), (*got, *b)))
