@@ -214,7 +214,7 @@ __device__ __forceinline__ void wave_fence() {
 // tiles in turn, each with LDS of its own and no barrier, and merge at the
 // end.  With one chunk the result is final; otherwise the maximum, sum and
 // float32 output go to `part` for k_attn_merge.  Bound by the cache: 32 caches
-// of up to 16384 keys, 8 heads of 128, capped scores: 286 us, 5.6 TB/s of reads
+// of up to 16384 keys, 8 heads of 128, capped scores: 288 us, 5.6 TB/s of reads
 // (a kernel that only reads them in this order: 6.0).
 template <int DP, int NW, int MOD>
 __global__ __launch_bounds__(64 * NW, 1) void k_attn_split(const AttnArgs) {
