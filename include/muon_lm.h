@@ -1,8 +1,8 @@
 /*
  * muon_lm.h - the language-model operators of libmuon.so (MI355X, gfx950):
- * attention with its gradients, the norm and rotation of query and key heads
- * with its gradients, and the embedding with its gradient.  They compute the
- * model around the Muon step of muon.h.
+ * attention, the norm and rotation of query and key heads, the embedding, the
+ * gated feed-forward block, the norms around a block and dropout, with their
+ * gradients.  They compute the model around the Muon step of muon.h.
  *
  * Conventions (those of muon.h)
  *  - Device pointers; the caller owns every buffer and the workspace (aligned
@@ -162,6 +162,129 @@ size_t muon_embedding_backward_workspace_size(int64_t n, int64_t vocab, int64_t 
 int muon_embedding_backward(const void *tokens, int token_bytes, const void *dout, int dout_type, void *dtable,
                             int table_type, int64_t n, int64_t vocab, int64_t width, float scale, void *workspace,
                             size_t workspace_bytes, void *stream);
+
+/*
+ * Dropout from a counter-based generator; no mask is stored.  Element i of n
+ * has 16 random bits: half i % 8 (low halves first) of the four words of
+ * Philox4x32-10 under the key `seed`, for the counter offset + i / 8.  With t =
+ * round(65536 p) it is dropped (0, whatever x holds) where its bits are below
+ * t, else multiplied by 65536 / (65536 - t), in float32, rounded once.  The
+ * gradient is the same call on the gradient of `out`.
+ *  state : NULL, or (seed, block) on the device, read by the kernel: the seed
+ *          used, and what is added to offset.  A captured graph whose state
+ *          the program advances drops other elements at every replay.
+ *  x, out: [n] of dtype, contiguous; out may be x.
+ * A call uses (n + 7) / 8 blocks.  Errors: MUON_ERR_INVALID_ARG (p outside 0 ..
+ * 1, null or misaligned pointers, a negative n), MUON_ERR_UNSUPPORTED (n above
+ * 2^41).
+ */
+int muon_dropout(const void *x, void *out, int64_t n, int dtype, double p, uint64_t seed, uint64_t offset,
+                 const int64_t *state, void *stream);
+
+/* Largest width of the norms around a block. */
+#define MUON_RESIDUAL_NORM_MAX_WIDTH 8192
+
+/* Which gate a block has: none, a value per channel ([width] float32), per
+ * sequence and channel ([batch][width] float32), or per element (of block_type). */
+typedef enum { MUON_GATE_NONE = 0, MUON_GATE_CHANNEL = 1, MUON_GATE_SEQUENCE = 2, MUON_GATE_FULL = 3 } muon_gate_kind;
+
+/*
+ * The norms before and after a block of a decoder layer, its dropout, gate and
+ * residual scale, in one pass over each row (a token):
+ *   n     = y / sqrt(mean(y^2) + eps) post_weight      post; else n = y
+ *   n     = dropout of n                               (muon_dropout's, element row width + column)
+ *   x_out = residual_scale x + gate n
+ *   z     = x_out / sqrt(mean(x_out^2) + eps) pre_weight
+ * in float32; x_out and z are rounded once each (z is computed from x_out
+ * before its rounding).  Without a block (has_block 0) x_out = residual_scale x.
+ *
+ * Backward, from dz and dx_out (gradients of z and of x_out) and the x_out
+ * that the forward pass returned: dx, dy and the gradients of gate,
+ * residual_scale and the weights; sums over rows are float32 in one order.
+ * Given NULL, weights and residual_scale are ones and have no gradient; a
+ * weight's gradient is not computed where its pointer is NULL.
+ */
+typedef struct muon_residual_norm_args {
+    const void *x;        /* [batch s][width] of stream_type; backward: read for dresidual_scale only */
+    const void *y;        /* the block's output, of block_type */
+    const void *gate;     /* as gate_kind says */
+    const float *residual_scale, *post_weight, *pre_weight; /* [width], or NULL */
+    void *x_out;          /* stream_type; forward: written, contiguous, or NULL: not wanted; backward: read */
+    void *z;              /* forward: of block_type, contiguous */
+    const void *dz;       /* backward: of block_type */
+    const void *dx_out;   /* backward: of stream_type, or NULL: zeros */
+    void *dx, *dy;        /* backward: of stream_type and block_type, contiguous */
+    void *dgate;          /* backward: shaped and typed as gate, contiguous */
+    float *dresidual_scale, *dpost_weight, *dpre_weight;    /* backward: [width], or NULL */
+    int64_t x_stride, y_stride, gate_stride, x_out_stride, dz_stride, dx_out_stride; /* between rows, in elements */
+    int64_t batch, s, width;
+    int64_t stream_type, block_type; /* muon_dtype; a float32 block needs a float32 stream */
+    int64_t has_block, post, gate_kind;
+    double eps, p;
+    uint64_t seed, offset;
+    const int64_t *state; /* as muon_dropout's */
+} muon_residual_norm_args;
+
+/* Bytes of workspace of the backward pass (at least 256; 0 for invalid sizes). */
+size_t muon_residual_norm_backward_workspace_size(const muon_residual_norm_args *args);
+/*
+ * x_out may be x, and z may be y (the same type and stride, width).  Backward:
+ * dx may be dx_out, and dy may be dz or y.
+ * Errors: MUON_ERR_INVALID_ARG (null or misaligned pointers, negative sizes or
+ * strides, p outside 0 .. 1, a negative eps, unknown types, a gate, post norm
+ * or dropout without a block, a weight without its norm), MUON_ERR_UNSUPPORTED
+ * (a width above the largest, a size of 2^29 or more, a float32 block on a
+ * bfloat16 stream, more than 2^20 sequences with a gate each),
+ * MUON_ERR_WORKSPACE.  A width that is a multiple of 8 with rows aligned to 16
+ * bytes runs fastest.
+ */
+int muon_residual_norm(const muon_residual_norm_args *args, void *stream);
+int muon_residual_norm_backward(const muon_residual_norm_args *args, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/* silu: g / (1 + e^-g); gelu: g (1 + erf(g / sqrt 2)) / 2; gelu_tanh: its
+ * approximation g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2; relu. */
+typedef enum { MUON_SILU = 0, MUON_GELU = 1, MUON_GELU_TANH = 2, MUON_RELU = 3 } muon_activation;
+
+/*
+ * The gated feed-forward block, in bfloat16 with float32 sums:
+ *   gate = x w_gate^T, up = x w_up^T, h = activation(gate) up, out = h w_down^T
+ * and its gradients from dout.  h, gate and up are rounded to bfloat16 once
+ * each (h from the unrounded gate and up), and so are the gradients of gate
+ * and up; everything else is float32, rounded once.
+ */
+typedef struct muon_feed_forward_args {
+    const uint16_t *x;      /* [tokens][width], bfloat16 */
+    const uint16_t *w_gate; /* [hidden][width] */
+    const uint16_t *w_up;   /* [hidden][width] */
+    const uint16_t *w_down; /* [width][hidden] */
+    uint16_t *out;          /* forward: [tokens][width], contiguous */
+    uint16_t *kept;         /* [3][tokens][hidden], contiguous: gate, up and h.  Forward: NULL where no backward
+                             * pass follows; backward: as the forward pass left it */
+    const uint16_t *dout;   /* backward: [tokens][width] */
+    uint16_t *dx;           /* backward: [tokens][width], contiguous */
+    void *dw_gate, *dw_up, *dw_down; /* backward: shaped as the matrices, of dw_type, contiguous */
+    int64_t x_stride, w_stride, w_down_stride, dout_stride; /* between rows, in elements (w_stride: w_gate and w_up) */
+    int64_t tokens, width, hidden;
+    int64_t activation;     /* muon_activation */
+    int64_t dw_type;        /* muon_dtype */
+} muon_feed_forward_args;
+
+/* Bytes of workspace (at least 256; 0 for invalid sizes). */
+size_t muon_feed_forward_workspace_size(const muon_feed_forward_args *args);
+size_t muon_feed_forward_backward_workspace_size(const muon_feed_forward_args *args);
+
+/*
+ * Errors: MUON_ERR_INVALID_ARG (null pointers, a negative size, pointers not
+ * aligned to 16 bytes, strides that are no multiple of 8 or shorter than a
+ * row, unknown activation or type), MUON_ERR_UNSUPPORTED (width or hidden not a multiple of 8, strides
+ * or widths of 2^21 or more, 2^29 tokens or more, too many tiles),
+ * MUON_ERR_WORKSPACE.
+ */
+int muon_feed_forward(const muon_feed_forward_args *args, void *workspace, size_t workspace_bytes, void *stream);
+/* dx, dw_gate, dw_up and dw_down; no tokens give zeros for the matrices. */
+int muon_feed_forward_backward(const muon_feed_forward_args *args, void *workspace, size_t workspace_bytes,
+                               void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,467 @@
+// C ABI of the operators of a decoder layer: validation, plans and workspace
+// layout (declared and documented in include/muon_lm.h).
+#include <math.h>
+
+#include "../../include/muon_lm.h"
+#include "layer_common.hpp"
+#include "lm_host.hpp"
+
+namespace muon {
+
+namespace {
+
+int64_t type_bytes(int64_t dtype) { return dtype == MUON_BF16 ? 2 : 4; }
+bool known_type(int64_t dtype) { return dtype == MUON_F32 || dtype == MUON_BF16; }
+
+// --------------------------------------------------------------- dropout
+
+int make_drop(double p, uint64_t seed, uint64_t offset, const int64_t* state, DropState& d) {
+    if (!(p >= 0.0 && p <= 1.0)) return refuse(MUON_ERR_INVALID_ARG, "p must be within 0 .. 1");
+    if (!aligned(state, 8)) return refuse(MUON_ERR_INVALID_ARG, "state is not aligned to 8 bytes");
+    d.seed = seed;
+    d.offset = offset;
+    d.state = state;
+    d.threshold = static_cast<uint32_t>(floor(p * 65536.0 + 0.5));
+    d.factor = d.threshold < 65536 ? static_cast<float>(65536.0 / (65536 - static_cast<int>(d.threshold))) : 0.0f;
+    return MUON_OK;
+}
+
+// ---------------------------------------------------- norms around a block
+
+int check_resid(const muon_residual_norm_args* x) {
+    if (!x) return refuse(MUON_ERR_INVALID_ARG, "null arguments");
+    if (x->batch < 0 || x->s < 0) return refuse(MUON_ERR_INVALID_ARG, "negative size");
+    if (x->width <= 0 || x->width > MUON_RESIDUAL_NORM_MAX_WIDTH)
+        return refuse(MUON_ERR_UNSUPPORTED, "width %lld is not within 1 .. %d", (long long)x->width,
+                      MUON_RESIDUAL_NORM_MAX_WIDTH);
+    if (x->batch >= kMaxSeq || x->s >= kMaxSeq) return refuse(MUON_ERR_UNSUPPORTED, "a size of 2^29 or more");
+    const int64_t n = times(times(x->batch, x->s), x->width);
+    if (n < 0) return refuse(MUON_ERR_UNSUPPORTED, "too many rows");
+    if (!known_type(x->stream_type) || !known_type(x->block_type)) return refuse(MUON_ERR_INVALID_ARG, "unknown dtype");
+    if (x->stream_type == MUON_BF16 && x->block_type == MUON_F32)
+        return refuse(MUON_ERR_UNSUPPORTED, "a float32 block on a bfloat16 stream");
+    if (x->gate_kind < GATE_NONE || x->gate_kind > GATE_FULL) return refuse(MUON_ERR_INVALID_ARG, "unknown gate_kind");
+    if (x->gate_kind == GATE_SEQUENCE && x->batch > (int64_t{1} << 20))
+        return refuse(MUON_ERR_UNSUPPORTED, "more than 2^20 sequences with a gate each");
+    if (!(x->eps >= 0.0) || !isfinite(static_cast<float>(x->eps)))
+        return refuse(MUON_ERR_INVALID_ARG, "eps must be >= 0 and finite");
+    return MUON_OK;
+}
+
+struct ResidPlan {
+    int waves, pieces, chunks, per;
+    int64_t blocks, groups;
+    size_t off_gate, bytes;
+};
+
+// Waves that hold a row: 1 up to 1024 values, then as many as keep it at two
+// pieces of 8 a lane (single values: at most 16 a lane).
+//
+// Backward, a workgroup leaves a row of sums, which are written and read again:
+// 4 workgroups a CU are enough to fill the memory's queues.
+ResidPlan plan_resid(const muon_residual_norm_args* x, bool vector, bool backward) {
+    ResidPlan p{};
+    p.pieces = 2;
+    if (vector) {
+        const int64_t n = x->width / 8;
+        p.waves = n <= 128 ? 1 : n <= 256 ? 2 : n <= 512 ? 4 : 8;
+        if (n <= 64) p.pieces = 1;
+    } else {
+        p.waves = x->width <= 256 ? 1 : x->width <= 2048 ? 4 : 8;
+    }
+    const int64_t rows = x->batch * x->s, per_block = p.waves >= 4 ? 1 : 4 / p.waves;
+    p.chunks = p.per = 1;
+    p.groups = 1;
+    if (!backward) {
+        const int64_t n = div_up(rows, per_block), most = p.waves == 8 ? 1024 : 2048;
+        p.blocks = n < most ? n : most;
+        p.bytes = 256;
+        return p;
+    }
+    const int64_t most = p.waves == 8 ? 512 : 1024;
+    const bool by_sequence = x->gate_kind == GATE_SEQUENCE;
+    p.groups = by_sequence ? x->batch : 1;
+    const int64_t n = div_up(by_sequence ? x->s : rows, per_block);
+    if (p.groups >= most) {
+        p.per = static_cast<int>(div_up(p.groups, most));
+        p.blocks = div_up(p.groups, p.per);
+    } else if (p.groups > 0) {
+        const int64_t c = most / p.groups;
+        p.chunks = static_cast<int>(n < 1 ? 1 : n < c ? n : c);
+        p.blocks = p.groups * p.chunks;
+    }
+    p.off_gate = align256(static_cast<size_t>(p.blocks) * 4 * x->width * sizeof(float));
+    p.bytes = p.off_gate;
+    if (by_sequence && p.chunks > 1) p.bytes += align256(static_cast<size_t>(p.blocks) * x->width * sizeof(float));
+    if (p.bytes < 256) p.bytes = 256;
+    return p;
+}
+
+int run_resid(const muon_residual_norm_args* x, bool backward, void* ws, size_t ws_bytes, hipStream_t stream) {
+    if (int st = check_resid(x)) return st;
+    ResidArgs a{};
+    if (int st = make_drop(x->p, x->seed, x->offset, x->state, a.drop)) return st;
+    const int64_t rows = x->batch * x->s, xb = type_bytes(x->stream_type), yb = type_bytes(x->block_type);
+    const bool block = x->has_block != 0;
+    if (!block && (x->gate_kind != GATE_NONE || x->post || a.drop.threshold))
+        return refuse(MUON_ERR_INVALID_ARG, "a gate, post norm or dropout without a block's output");
+    if (!x->post && (x->post_weight || x->dpost_weight))
+        return refuse(MUON_ERR_INVALID_ARG, "a weight of the post norm without that norm");
+    bool vec = x->width % 8 == 0;
+    const char* bad = nullptr;
+    // a tensor of rows that the call reads or writes
+    auto row = [&](const char* name, const void* p, int64_t bytes, int64_t stride) {
+        if (rows == 0 || bad) return;
+        if (!p || !aligned(p, bytes) || (rows > 1 && stride < 0)) bad = name;
+        vec = vec && aligned(p, 16) && (rows <= 1 || stride % 8 == 0);
+    };
+    const bool full = x->gate_kind == GATE_FULL;
+    if (!backward) {
+        row("x", x->x, xb, x->x_stride);
+        if (block) row("y", x->y, yb, x->y_stride);
+        if (x->x_out) row("x_out", x->x_out, xb, 0);
+        row("z", x->z, yb, 0);
+    } else {
+        row("x_out", x->x_out, xb, x->x_out_stride);
+        row("dz", x->dz, yb, x->dz_stride);
+        if (x->dx_out) row("dx_out", x->dx_out, xb, x->dx_out_stride);
+        if (x->dresidual_scale) row("x", x->x, xb, x->x_stride);
+        if (block) row("y", x->y, yb, x->y_stride);
+        row("dx", x->dx, xb, 0);
+        if (block) row("dy", x->dy, yb, 0);
+        if (full) row("dgate", x->dgate, yb, 0);
+    }
+    if (full) row("gate", x->gate, yb, x->gate_stride);
+    if (bad) return refuse(MUON_ERR_INVALID_ARG, "%s is null or not aligned to its type, or its stride is negative", bad);
+    if (x->gate_kind != GATE_NONE && !full && !x->gate) return refuse(MUON_ERR_INVALID_ARG, "gate is null");
+    if (backward && (x->gate_kind == GATE_CHANNEL || x->gate_kind == GATE_SEQUENCE) && !x->dgate)
+        return refuse(MUON_ERR_INVALID_ARG, "dgate is null");
+    if (backward && x->dresidual_scale && !x->residual_scale)
+        return refuse(MUON_ERR_INVALID_ARG, "dresidual_scale without residual_scale");
+    for (const void* p : {static_cast<const void*>(x->residual_scale), static_cast<const void*>(x->post_weight),
+                          static_cast<const void*>(x->pre_weight), static_cast<const void*>(full ? nullptr : x->gate),
+                          static_cast<const void*>(backward ? x->dresidual_scale : nullptr),
+                          static_cast<const void*>(backward ? x->dpost_weight : nullptr),
+                          static_cast<const void*>(backward ? x->dpre_weight : nullptr),
+                          static_cast<const void*>(backward && !full ? x->dgate : nullptr)})
+        if (!aligned(p, 4)) return refuse(MUON_ERR_INVALID_ARG, "a vector is not aligned to 4 bytes");
+    if (backward)
+        if (int st = check_workspace(ws, ws_bytes, muon_residual_norm_backward_workspace_size(x))) return st;
+    if (!backward && rows == 0) return done();
+    const ResidPlan p = plan_resid(x, vec, backward);
+    auto step = [&](int64_t stride) { return rows > 1 ? stride : 0; };
+    a.x = x->x;
+    a.y = block ? x->y : nullptr;
+    a.gate = x->gate;
+    a.x_s = step(x->x_stride);
+    a.y_s = step(x->y_stride);
+    a.g_s = step(x->gate_stride);
+    if (backward) {
+        a.xo = x->x_out;
+        a.dz = x->dz;
+        a.dxo = x->dx_out;
+        a.xo_s = step(x->x_out_stride);
+        a.dz_s = step(x->dz_stride);
+        a.dxo_s = step(x->dx_out_stride);
+        a.dx = x->dx;
+        a.dy = x->dy;
+        a.dgate = x->gate_kind == GATE_NONE ? nullptr : x->dgate;
+        a.dscale = x->dresidual_scale;
+        a.dpostw = x->dpost_weight;
+        a.dprew = x->dpre_weight;
+        a.part = static_cast<float*>(ws);
+        if (x->gate_kind == GATE_SEQUENCE && p.chunks > 1)
+            a.gate_part = reinterpret_cast<float*>(static_cast<char*>(ws) + p.off_gate);
+    } else {
+        a.x_out = x->x_out;
+        a.z = x->z;
+    }
+    a.scale = x->residual_scale;
+    a.postw = x->post_weight;
+    a.prew = x->pre_weight;
+    a.rows = rows;
+    a.s = x->s;
+    a.width = static_cast<int>(x->width);
+    a.x_type = static_cast<int>(x->stream_type);
+    a.y_type = static_cast<int>(x->block_type);
+    a.gate_kind = static_cast<int>(x->gate_kind);
+    a.post = x->post != 0;
+    a.vector = vec;
+    a.waves = p.waves;
+    a.pieces = p.pieces;
+    a.blocks = p.blocks;
+    a.groups = p.groups;
+    a.chunks = p.chunks;
+    a.per = p.per;
+    a.eps = static_cast<float>(x->eps);
+    const int st = launched(backward ? launch_resid_norm_bwd(a, stream) : launch_resid_norm(a, stream), "norms of a block");
+    return st ? st : done();
+}
+
+// ----------------------------------------------------------- feed-forward
+
+constexpr int64_t kMaxFfnStride = int64_t{1} << 21;  // elements: a tile's offsets stay below 2^31 bytes
+constexpr int64_t kMaxFfnTiles = (int64_t{1} << 23) - 1;  // workgroups of 512 threads below 2^32 threads
+
+int check_ffn(const muon_feed_forward_args* x) {
+    if (!x) return refuse(MUON_ERR_INVALID_ARG, "null arguments");
+    if (x->tokens < 0) return refuse(MUON_ERR_INVALID_ARG, "negative size");
+    if (x->width <= 0 || x->hidden <= 0 || x->width % 8 != 0 || x->hidden % 8 != 0)
+        return refuse(MUON_ERR_UNSUPPORTED, "width (%lld) and hidden (%lld) must be positive multiples of 8",
+                      (long long)x->width, (long long)x->hidden);
+    if (x->width >= kMaxFfnStride || x->hidden >= kMaxFfnStride)
+        return refuse(MUON_ERR_UNSUPPORTED, "a width of 2^21 or more");
+    if (x->tokens >= kMaxSeq) return refuse(MUON_ERR_UNSUPPORTED, "2^29 tokens or more");
+    if (x->activation < ACT_SILU || x->activation > ACT_RELU) return refuse(MUON_ERR_INVALID_ARG, "unknown activation");
+    const int64_t most = x->width > x->hidden ? x->width : x->hidden;
+    if (div_up(x->tokens, 128) * div_up(most, 64) > kMaxFfnTiles || div_up(most, 128) * div_up(most, 128) * 3 > kMaxFfnTiles)
+        return refuse(MUON_ERR_UNSUPPORTED, "too many tokens or columns");
+    return MUON_OK;
+}
+
+// Rows of a matrix that the matrix cores' loads read 16 bytes at a time.
+int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t stride) {
+    if (rows == 0) return MUON_OK;
+    if (!p) return refuse(MUON_ERR_INVALID_ARG, "%s is null", name);
+    if (!aligned(p, 16)) return refuse(MUON_ERR_INVALID_ARG, "%s is not aligned to 16 bytes", name);
+    // (rows that share memory would put values where the loads expect the end)
+    if (rows > 1 && (stride < cols || stride % 8 != 0))
+        return refuse(MUON_ERR_INVALID_ARG, "%s: stride %lld is not a multiple of 8 elements from %lld on", name,
+                      (long long)stride, (long long)cols);
+    if (rows > 1 && stride >= kMaxFfnStride) return refuse(MUON_ERR_UNSUPPORTED, "%s: row stride of 2^21 elements or more", name);
+    return MUON_OK;
+}
+
+struct FfnPlan {
+    int tile, splits;
+};
+
+// The tile and the number of splits of K that take the least time: rounds of
+// workgroups over the CUs times the steps of one, and the sums of the splits.
+FfnPlan plan_ffn(int64_t m, int64_t n, int64_t steps, int count, bool may_split) {
+    FfnPlan best{128, 1};
+    double least = 1e300;
+    for (const int tile : {256, 128}) {
+        const int64_t tiles = div_up(m, tile) * div_up(n, tile) * count, slots = tile == 256 ? 256 : 512;
+        // microseconds: a step of all workgroups that a CU holds, and what a
+        // workgroup spends before and after its steps
+        const double step = tile == 256 ? 1.8 : 1.0, over = tile == 256 ? 6.0 : 4.0;
+        for (int s = 1; s <= 32; ++s) {
+            if (s > 1 && (!may_split || s > steps / 4)) break;
+            if (tiles * s > kMaxFfnTiles) break;
+            double t = static_cast<double>(div_up(tiles * s, slots)) * (static_cast<double>(div_up(steps, s)) * step + over);
+            if (s > 1) t += 4.0 + static_cast<double>(count) * m * n * s * 8.0 / 4e6;
+            if (t < least) {
+                least = t;
+                best.tile = tile;
+                best.splits = s;
+            }
+        }
+    }
+    return best;
+}
+
+constexpr int64_t kBkSteps = 64;
+FfnPlan plan_gated(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, 2 * x->hidden, div_up(x->width, kBkSteps), 1, false); }
+FfnPlan plan_down(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, x->width, div_up(x->hidden, kBkSteps), 1, true); }
+FfnPlan plan_hidden(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, x->hidden, div_up(x->width, kBkSteps), 1, false); }
+FfnPlan plan_input(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, x->width, 2 * div_up(x->hidden, kBkSteps), 1, true); }
+FfnPlan plan_weights(const muon_feed_forward_args* x) { return plan_ffn(x->hidden, x->width, div_up(x->tokens, kBkSteps), 3, true); }
+
+size_t part_bytes(const FfnPlan& p, int64_t m, int64_t n, int count) {
+    return p.splits > 1 ? align256(static_cast<size_t>(p.splits) * m * n * sizeof(float)) * count : 0;
+}
+size_t hidden_bytes(const muon_feed_forward_args* x) { return align256(static_cast<size_t>(x->tokens) * x->hidden * 2); }
+
+size_t forward_bytes(const muon_feed_forward_args* x) {
+    // h, also where `kept` holds it: the size does not depend on the pointers
+    const size_t n = hidden_bytes(x) + part_bytes(plan_down(x), x->tokens, x->width, 1);
+    return n > 256 ? n : 256;
+}
+size_t backward_bytes(const muon_feed_forward_args* x) {
+    const size_t a = part_bytes(plan_input(x), x->tokens, x->width, 1), b = part_bytes(plan_weights(x), x->hidden, x->width, 3);
+    const size_t n = 2 * hidden_bytes(x) + (a > b ? a : b);
+    return n > 256 ? n : 256;
+}
+
+// One product of a launch; first: tiles of those before it.
+void add_seg(FfnGemm& g, int tile, bool gated, const bf16_t* p0, const bf16_t* p1, int64_t ldp, const bf16_t* q0,
+             const bf16_t* q1, int64_t ldq, int64_t m, int64_t n, void* out, float* part) {
+    FfnSeg& s = g.seg[g.nseg++];
+    s.p[0] = p0;
+    s.p[1] = p1;
+    s.q[0] = q0;
+    s.q[1] = q1;
+    s.ldp = ldp;
+    s.ldq = ldq;
+    s.m = static_cast<int>(m);
+    s.n = static_cast<int>(n);
+    s.tiles_m = static_cast<int>(div_up(m, tile));
+    s.tiles_n = static_cast<int>(div_up(n, gated ? tile / 2 : tile));
+    s.first = g.tiles;
+    s.out = out;
+    s.part = part;
+    g.tiles += s.tiles_m * s.tiles_n;
+}
+void set_steps(FfnGemm& g, const FfnPlan& p, int64_t k, int phases) {
+    g.k = k;
+    g.phases = phases;
+    const int64_t steps = div_up(k, kBkSteps) * phases;
+    g.split_steps = static_cast<int>(div_up(steps, p.splits));
+    g.splits = p.splits;
+    g.band = 8;
+}
+
+}  // namespace
+
+}  // namespace muon
+
+extern "C" {
+
+int muon_dropout(const void* x, void* out, int64_t n, int dtype, double p, uint64_t seed, uint64_t offset,
+                 const int64_t* state, void* stream) {
+    using namespace muon;
+    if (n < 0) return refuse(MUON_ERR_INVALID_ARG, "negative size");
+    if (!known_type(dtype)) return refuse(MUON_ERR_INVALID_ARG, "unknown dtype");
+    if (n > (int64_t{1} << 41)) return refuse(MUON_ERR_UNSUPPORTED, "more than 2^41 elements");
+    DropArgs a{};
+    if (int st = make_drop(p, seed, offset, state, a.drop)) return st;
+    if (n == 0) return done();
+    if (!x || !out) return refuse(MUON_ERR_INVALID_ARG, "null pointer argument");
+    if (!aligned(x, type_bytes(dtype)) || !aligned(out, type_bytes(dtype)))
+        return refuse(MUON_ERR_INVALID_ARG, "a tensor is not aligned to its type");
+    a.x = x;
+    a.out = out;
+    a.n = n;
+    a.type = dtype;
+    a.vector = aligned(x, 16) && aligned(out, 16);
+    const int st = launched(launch_dropout(a, static_cast<hipStream_t>(stream)), "dropout");
+    return st ? st : done();
+}
+
+size_t muon_residual_norm_backward_workspace_size(const muon_residual_norm_args* x) {
+    using namespace muon;
+    if (check_resid(x)) return 0;
+    // the pointers' alignment, which decides between the two plans, is not looked at here
+    size_t n = 256;
+    for (const bool vector : {false, true}) {
+        const size_t bytes = plan_resid(x, vector, true).bytes;
+        if (bytes > n) n = bytes;
+    }
+    return n;
+}
+
+int muon_residual_norm(const muon_residual_norm_args* x, void* stream) {
+    return muon::run_resid(x, false, nullptr, 0, static_cast<hipStream_t>(stream));
+}
+
+int muon_residual_norm_backward(const muon_residual_norm_args* x, void* ws, size_t ws_bytes, void* stream) {
+    return muon::run_resid(x, true, ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+size_t muon_feed_forward_workspace_size(const muon_feed_forward_args* x) {
+    using namespace muon;
+    return check_ffn(x) ? 0 : forward_bytes(x);
+}
+
+size_t muon_feed_forward_backward_workspace_size(const muon_feed_forward_args* x) {
+    using namespace muon;
+    return check_ffn(x) ? 0 : backward_bytes(x);
+}
+
+int muon_feed_forward(const muon_feed_forward_args* x, void* ws, size_t ws_bytes, void* stream) {
+    using namespace muon;
+    if (int st = check_ffn(x)) return st;
+    if (int st = check_matrix("x", x->x, x->tokens, x->width, x->x_stride)) return st;
+    if (int st = check_matrix("w_gate", x->w_gate, x->hidden, x->width, x->w_stride)) return st;
+    if (int st = check_matrix("w_up", x->w_up, x->hidden, x->width, x->w_stride)) return st;
+    if (int st = check_matrix("w_down", x->w_down, x->width, x->hidden, x->w_down_stride)) return st;
+    if (int st = check_matrix("out", x->out, x->tokens, x->width, x->width)) return st;
+    if (!aligned(x->kept, 16)) return refuse(MUON_ERR_INVALID_ARG, "kept is not aligned to 16 bytes");
+    if (int st = check_workspace(ws, ws_bytes, forward_bytes(x))) return st;
+    if (x->tokens == 0) return done();
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t t = x->tokens, h = x->hidden, w = x->width;
+    const int64_t x_step = t > 1 ? x->x_stride : w;  // (of one row it may be anything)
+    bf16_t* hid = x->kept ? x->kept + 2 * t * h : static_cast<bf16_t*>(ws);
+    {
+        const FfnPlan p = plan_gated(x);
+        FfnGemm g{};
+        add_seg(g, p.tile, true, x->x, nullptr, x_step, x->w_gate, x->w_up, x->w_stride, t, h, hid, nullptr);
+        set_steps(g, p, w, 1);
+        g.act = static_cast<int>(x->activation);
+        if (x->kept) {
+            g.gate = x->kept;
+            g.up = x->kept + t * h;
+        }
+        if (int st = launched(launch_ffn(FFN_GATED, p.tile, g, s), "gate and up projections")) return st;
+    }
+    {
+        const FfnPlan p = plan_down(x);
+        FfnGemm g{};
+        float* part = p.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + hidden_bytes(x)) : nullptr;
+        add_seg(g, p.tile, false, hid, nullptr, h, x->w_down, nullptr, x->w_down_stride, t, w, x->out, part);
+        set_steps(g, p, h, 1);
+        if (int st = launched(launch_ffn(FFN_PLAIN, p.tile, g, s), "down projection")) return st;
+    }
+    return done();
+}
+
+int muon_feed_forward_backward(const muon_feed_forward_args* x, void* ws, size_t ws_bytes, void* stream) {
+    using namespace muon;
+    if (int st = check_ffn(x)) return st;
+    if (int st = check_matrix("x", x->x, x->tokens, x->width, x->x_stride)) return st;
+    if (int st = check_matrix("dout", x->dout, x->tokens, x->width, x->dout_stride)) return st;
+    if (int st = check_matrix("w_gate", x->w_gate, x->hidden, x->width, x->w_stride)) return st;
+    if (int st = check_matrix("w_up", x->w_up, x->hidden, x->width, x->w_stride)) return st;
+    if (int st = check_matrix("w_down", x->w_down, x->width, x->hidden, x->w_down_stride)) return st;
+    if (int st = check_matrix("dx", x->dx, x->tokens, x->width, x->width)) return st;
+    if (int st = check_matrix("kept", x->kept, x->tokens, x->hidden, x->hidden)) return st;
+    if (int st = check_matrix("dw_gate", x->dw_gate, x->hidden, x->width, x->width)) return st;
+    if (int st = check_matrix("dw_up", x->dw_up, x->hidden, x->width, x->width)) return st;
+    if (int st = check_matrix("dw_down", x->dw_down, x->width, x->hidden, x->hidden)) return st;
+    if (!known_type(x->dw_type)) return refuse(MUON_ERR_INVALID_ARG, "unknown dtype");
+    if (int st = check_workspace(ws, ws_bytes, backward_bytes(x))) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t t = x->tokens, h = x->hidden, w = x->width;
+    const int64_t x_step = t > 1 ? x->x_stride : w;  // (of one row it may be anything)
+    const int64_t do_step = t > 1 ? x->dout_stride : w;
+    char* at = static_cast<char*>(ws);
+    bf16_t* dgate = reinterpret_cast<bf16_t*>(at);
+    bf16_t* dup = reinterpret_cast<bf16_t*>(at + hidden_bytes(x));
+    float* part = reinterpret_cast<float*>(at + 2 * hidden_bytes(x));
+    if (t > 0) {
+        const FfnPlan p = plan_hidden(x);
+        FfnGemm g{};
+        add_seg(g, p.tile, false, x->dout, nullptr, do_step, x->w_down, nullptr, x->w_down_stride, t, h, nullptr, nullptr);
+        set_steps(g, p, w, 1);
+        g.act = static_cast<int>(x->activation);
+        g.gate = x->kept;
+        g.up = x->kept + t * h;
+        g.dgate = dgate;
+        g.dup = dup;
+        if (int st = launched(launch_ffn(FFN_HIDDEN, p.tile, g, s), "gradient of the hidden values")) return st;
+    }
+    if (t > 0) {
+        const FfnPlan p = plan_input(x);
+        FfnGemm g{};
+        add_seg(g, p.tile, false, dgate, dup, h, x->w_gate, x->w_up, x->w_stride, t, w, x->dx, p.splits > 1 ? part : nullptr);
+        set_steps(g, p, h, 2);
+        if (int st = launched(launch_ffn(FFN_INPUT, p.tile, g, s), "gradient of x")) return st;
+    }
+    {
+        const FfnPlan p = plan_weights(x);
+        const size_t one = p.splits > 1 ? part_bytes(p, h, w, 1) / sizeof(float) : 0;
+        auto place = [&](int i) { return p.splits > 1 ? part + i * one : nullptr; };
+        FfnGemm g{};
+        add_seg(g, p.tile, false, dgate, nullptr, h, x->x, nullptr, x_step, h, w, x->dw_gate, place(0));
+        add_seg(g, p.tile, false, dup, nullptr, h, x->x, nullptr, x_step, h, w, x->dw_up, place(1));
+        add_seg(g, p.tile, false, x->dout, nullptr, do_step, x->kept + 2 * t * h, nullptr, h, w, h, x->dw_down, place(2));
+        set_steps(g, p, t, 1);
+        g.out_f32 = x->dw_type == MUON_F32;
+        if (int st = launched(launch_ffn(FFN_WEIGHTS, p.tile, g, s), "gradients of the matrices")) return st;
+    }
+    return done();
+}
+
+}  // extern "C"

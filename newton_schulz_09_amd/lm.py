@@ -1,6 +1,7 @@
 """Python binding of the language-model operators of libmuon.so (C ABI in
 include/muon_lm.h): attention, the norm and rotation of query and key heads,
-and the embedding, each with its gradients.
+the embedding, the gated feed-forward block, the norms around a block with its
+gate and residual scale, and dropout, each with its gradients.
 
 Argument checks and marshalling only; every step runs in the HIP kernels of
 the library.  Calls run on the current stream of the tensors' device and do
@@ -36,7 +37,15 @@ for _name, _res, _args in (
         ("muon_embedding", _int, [_vp, _int, _vp, _int, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _vp]),
         ("muon_embedding_backward_workspace_size", _sz, [_i64, _i64, _i64]),
         ("muon_embedding_backward", _int, [_vp, _int, _vp, _int, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _vp, _sz,
-                                           _vp])):
+                                           _vp]),
+        ("muon_dropout", _int, [_vp, _vp, _i64, _int, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, _vp, _vp]),
+        ("muon_residual_norm_backward_workspace_size", _sz, [_buf]),
+        ("muon_residual_norm", _int, [_buf, _vp]),
+        ("muon_residual_norm_backward", _int, [_buf, _vp, _sz, _vp]),
+        ("muon_feed_forward_workspace_size", _sz, [_buf]),
+        ("muon_feed_forward_backward_workspace_size", _sz, [_buf]),
+        ("muon_feed_forward", _int, [_buf, _vp, _sz, _vp]),
+        ("muon_feed_forward_backward", _int, [_buf, _vp, _sz, _vp])):
     getattr(_lib, _name).restype = _res
     getattr(_lib, _name).argtypes = _args
 
@@ -44,16 +53,24 @@ for _name, _res, _args in (
 EXPORTS = ("muon_attention_workspace_size", "muon_attention_backward_workspace_size", "muon_attention",
            "muon_attention_backward", "muon_qk_norm_rope_backward_workspace_size", "muon_qk_norm_rope",
            "muon_qk_norm_rope_backward", "muon_embedding", "muon_embedding_backward_workspace_size",
-           "muon_embedding_backward")
+           "muon_embedding_backward", "muon_dropout", "muon_residual_norm_backward_workspace_size",
+           "muon_residual_norm", "muon_residual_norm_backward", "muon_feed_forward_workspace_size",
+           "muon_feed_forward_backward_workspace_size", "muon_feed_forward", "muon_feed_forward_backward")
 #: Largest head sizes (MUON_ATTENTION_MAX_D, MUON_QK_NORM_MAX_D).
 ATTENTION_MAX_D = 128
 QK_NORM_MAX_D = 512
+#: Largest width of residual_norm (MUON_RESIDUAL_NORM_MAX_WIDTH).
+RESIDUAL_NORM_MAX_WIDTH = 8192
+#: Activations of feed_forward (muon_activation).
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
 
 _F32, _BF16 = torch.float32, torch.bfloat16
 _DTYPE = {_F32: muon.MUON_F32, _BF16: muon.MUON_BF16}
-# muon_attention_args and muon_qk_norm_rope_args: 8-byte fields throughout
+# the argument structures of muon_lm.h: 8-byte fields throughout
 _ATTN = struct.Struct("9Q15q2Qq3Q8q2d")
 _QK = struct.Struct("10Q12q2qQqQ3qqd")
+_RESID = struct.Struct("16Q6q3q2q3q2d3Q")
+_FFN = struct.Struct("11Q4q3q2q")
 
 
 # the current stream of a device as a number (0.1 us; a Stream object for it costs 2)
@@ -495,3 +512,347 @@ def embedding_backward(dout, tokens, vocab, scale=1.0, dtype=None, out=None, wor
     _call(dev, _lib.muon_embedding_backward, tokens.data_ptr(), token_bytes, dout.data_ptr(), _DTYPE[dout.dtype],
           out.data_ptr(), _DTYPE[out.dtype], n, vocab, width, float(scale), ptr, size)
     return out
+
+
+def _rows(t, name):
+    """The stride between the rows of the last dimension (any where there is at most one row)."""
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have a last dimension")
+    _last(t, name)
+    if t.is_contiguous():
+        return t.shape[-1]
+    step = count = None
+    for n, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step, count = stride, n
+        elif stride == step * count:
+            count *= n
+        else:
+            raise ValueError(f"the rows of {name} must be one stride apart (shape {tuple(t.shape)}, strides {t.stride()})")
+    return t.shape[-1] if step is None else step
+
+
+def _drop_args(p, seed, offset, dev):
+    """(p, seed, offset, address of the state) of dropout's generator."""
+    p = float(p)
+    if not 0.0 <= p <= 1.0:
+        raise ValueError(f"p must be within 0 .. 1 (got {p})")
+    offset = int(offset)
+    if isinstance(seed, torch.Tensor):
+        _exactly(seed, "seed", torch.int64, dev, (2,))
+        return p, 0, offset & 0xFFFFFFFFFFFFFFFF, seed.data_ptr()
+    return p, int(seed) & 0xFFFFFFFFFFFFFFFF, offset & 0xFFFFFFFFFFFFFFFF, 0
+
+
+def dropout(x, p, seed, offset=0, out=None):
+    """Drops elements of ``x`` (float32 or bfloat16, contiguous) with
+    probability t / 65536, t = round(65536 p), and multiplies the others by
+    65536 / (65536 - t).  Nothing is stored: element i (in memory order) is
+    dropped by 16 bits of Philox4x32-10 of ``seed`` and of block ``offset`` + i
+    / 8, so the gradient is ``dropout(dout, p, seed, offset)``, and a call uses
+    the ``(x.numel() + 7) // 8`` blocks from offset on.
+
+    ``seed`` is an integer, or an int64 tensor (seed, block) on x's device,
+    which the kernel reads: the seed, and what is added to ``offset``.  (A
+    captured graph whose tensor the program advances drops other elements at
+    every replay.)  ``out`` may be x itself; else it must not share memory with
+    x or seed."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    _tensor(x, "x", (_F32, _BF16), dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    p, key, first, state = _drop_args(p, seed, offset, dev)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _exactly(out, "out", x.dtype, dev, x.shape)
+        _apart(out, "out", (x, "x", True), (seed if state else None, "seed"))
+    _call(dev, _lib.muon_dropout, x.data_ptr(), out.data_ptr(), x.numel(), _DTYPE[x.dtype], p, key, first, state)
+    return out
+
+
+def _resid_args(x, y, gate, scale, post_weight, pre_weight, post, eps, p, seed, offset, dtype, forward, grads, dev):
+    """The checked arguments as muon_residual_norm_args.  x: the stream (or its
+    like, backward); forward: (x_out, z) tensors; grads: (dz, dx_out, x_out, x,
+    dx, dy, dgate, dscale, dpostw, dprew)."""
+    width = x.shape[-1]
+    if not 0 < width <= RESIDUAL_NORM_MAX_WIDTH:
+        raise ValueError(f"the width must be within 1 .. {RESIDUAL_NORM_MAX_WIDTH} (got {width})")
+    rows = x.numel() // width
+    batch, s = (x.shape[0], rows // x.shape[0] if x.shape[0] else 0) if x.dim() > 2 else (1, rows)
+    kind = g_ptr = g_step = 0
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        if y is None:
+            raise ValueError("a gate without a block's output")
+        if gate.shape == x.shape and gate.dim() > 1:
+            _tensor(gate, "gate", y.dtype, dev)
+            kind, g_step = 3, _rows(gate, "gate")
+        elif x.dim() > 2 and gate.dim() == 2:
+            _exactly(gate, "gate", _F32, dev, (batch, width))
+            kind = 2
+        else:
+            _exactly(gate, "gate", _F32, dev, (width,))
+            kind = 1
+        g_ptr = gate.data_ptr()
+    ptrs = []
+    for t, name in ((scale, "residual_scale"), (post_weight, "post_weight"), (pre_weight, "pre_weight")):
+        if t is not None:
+            _exactly(t, name, _F32, dev, (width,))
+        ptrs.append(0 if t is None else t.data_ptr())
+    p, key, first, state = _drop_args(p, seed, offset, dev)
+    if y is None:
+        post = False
+        if p:
+            raise ValueError("dropout without a block's output")
+    if post_weight is not None and not post:
+        raise ValueError("post_weight without the post norm")
+    y_ptr, y_step = (0, 0) if y is None else (y.data_ptr(), _rows(y, "y"))
+    a = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    r = lambda t, name: 0 if t is None else _rows(t, name)  # noqa: E731
+    if forward is not None:
+        x_out, z = forward
+        return _RESID.pack(x.data_ptr(), y_ptr, g_ptr, *ptrs, a(x_out), a(z), *(0,) * 8, _rows(x, "x"), y_step, g_step,
+                           0, 0, 0, batch, s, width, _DTYPE[x.dtype], _DTYPE[dtype], y is not None, bool(post), kind,
+                           float(eps), p, key, first, state)
+    dz, dx_out, x_out, x_in, dx, dy, dgate, dscale, dpostw, dprew = grads
+    return _RESID.pack(a(x_in), y_ptr, g_ptr, *ptrs, x_out.data_ptr(), 0, dz.data_ptr(), a(dx_out), a(dx), a(dy),
+                       a(dgate), a(dscale), a(dpostw), a(dprew), r(x_in, "x"), y_step, g_step, _rows(x_out, "x_out"),
+                       _rows(dz, "dz"), r(dx_out, "dx_out"), batch, s, width, _DTYPE[x_out.dtype], _DTYPE[dtype],
+                       y is not None, bool(post), kind, float(eps), p, key, first, state)
+
+
+def _resid_types(x, y, dev, name):
+    _tensor(x, name, (_F32, _BF16), dev)
+    if x.dim() < 1:
+        raise ValueError(f"{name} must have a last dimension")
+    if y is not None:
+        _tensor(y, "y", (_F32, _BF16), dev)
+        if y.shape != x.shape:
+            raise ValueError(f"y must have the shape of {name}, {tuple(x.shape)} (got {tuple(y.shape)})")
+        if y.dtype is _F32 and x.dtype is _BF16:
+            raise TypeError("a float32 block on a bfloat16 stream")
+
+
+def residual_norm(x, y=None, gate=None, residual_scale=None, post_weight=None, pre_weight=None, post=True, eps=1e-6,
+                  p=0.0, seed=0, offset=0, dtype=None, x_out=None, z_out=None):
+    """The norms before and after a block of a decoder layer, in one pass over
+    each row of the residual stream ``x`` (..., width) and the block's output
+    ``y`` (shaped as x; both float32 or bfloat16, a float32 y only with a
+    float32 x; rows one stride apart):
+
+        n     = y / sqrt(mean(y^2) + eps) post_weight     (``post``; else y)
+        n     = dropout(n, p, seed, offset)
+        x_out = residual_scale x + gate n
+        z     = x_out / sqrt(mean(x_out^2) + eps) pre_weight
+
+    Returns ``(x_out, z)``: the stream, of x's type, and the next block's input,
+    of y's.  ``gate`` is a float32 vector (width,), a float32 vector for each
+    sequence (x.shape[0], width) of an x of 3 dimensions or more, or a tensor
+    of y's shape and type; ``residual_scale`` and the weights are float32
+    vectors (width,).  What is None is one.  ``seed`` and ``offset`` as in
+    ``dropout``, elements counted in rows of x.
+
+    Without ``y``, as in front of the first block, z is the norm of
+    residual_scale x, of type ``dtype`` (default x's).
+
+    Computed in float32, rounded once.  Widths up to 8192; a multiple of 8 with
+    rows aligned to 16 bytes runs fastest.  ``x_out`` may be x and ``z_out`` y,
+    where those are contiguous; else given outputs must not share memory with
+    anything."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    _resid_types(x, y, dev, "x")
+    if y is not None:
+        if dtype is not None and dtype != y.dtype:
+            raise TypeError(f"z has y's type {y.dtype}, not {dtype}")
+        dtype = y.dtype
+    else:
+        dtype = x.dtype if dtype is None else dtype
+        _float_type(dtype, "dtype")
+        if dtype is _F32 and x.dtype is _BF16:
+            raise TypeError("a float32 block on a bfloat16 stream")
+    given = x_out, z_out
+    if x_out is None:
+        x_out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _exactly(x_out, "x_out", x.dtype, dev, x.shape)
+    if z_out is None:
+        z_out = torch.empty(x.shape, dtype=dtype, device=dev)
+    else:
+        _exactly(z_out, "z_out", dtype, dev, x.shape)
+    args = _resid_args(x, y, gate, residual_scale, post_weight, pre_weight, post, eps, p, seed, offset, dtype,
+                       (x_out, z_out), None, dev)
+    if given[0] is not None or given[1] is not None:
+        reads = ((gate, "gate"), (residual_scale, "residual_scale"), (post_weight, "post_weight"),
+                 (pre_weight, "pre_weight"), (seed if isinstance(seed, torch.Tensor) else None, "seed"))
+        if given[0] is not None:
+            _apart(x_out, "x_out", (x, "x", True), (y, "y"), *reads, (given[1], "z_out"))
+        if given[1] is not None:
+            _apart(z_out, "z_out", (x, "x"), (y, "y", True), *reads)
+    _call(dev, _lib.muon_residual_norm, args)
+    return x_out, z_out
+
+
+def residual_norm_backward(dz, dx_out, x_out, y=None, x=None, gate=None, residual_scale=None, post_weight=None,
+                           pre_weight=None, post=True, eps=1e-6, p=0.0, seed=0, offset=0, dx=None, dy=None,
+                           workspace=None):
+    """Gradients ``(dx, dy, dgate, dresidual_scale, dpost_weight, dpre_weight)``
+    of ``residual_norm`` from ``dz`` and ``dx_out`` (None: zeros), the gradients
+    of its results, its result ``x_out`` and its arguments; None for what was
+    not given.  ``x`` is needed with a residual_scale only.  dx has x_out's
+    type, dy and dz y's (without y dz is float32 or bfloat16), dgate is as gate,
+    the others are float32; sums over rows are float32, in one order.  A given
+    ``dx`` may be dx_out, and a given ``dy`` dz or y, where those are
+    contiguous; else they must not share memory with anything."""
+    if not isinstance(x_out, torch.Tensor):
+        raise TypeError("x_out must be a torch.Tensor")
+    dev = x_out.device
+    _resid_types(x_out, y, dev, "x_out")
+    _tensor(dz, "dz", (_F32, _BF16) if y is None else y.dtype, dev)
+    if dz.dtype is _F32 and x_out.dtype is _BF16:
+        raise TypeError("a float32 block on a bfloat16 stream")
+    x_in = None
+    if residual_scale is not None:
+        if x is None:
+            raise TypeError("x is needed for the gradient of residual_scale")
+        x_in = x
+    for t, name in ((dx_out, "dx_out"), (x_in, "x")):
+        if t is not None:
+            _tensor(t, name, x_out.dtype, dev)
+    for t, name in ((dz, "dz"), (dx_out, "dx_out"), (x_in, "x")):
+        if t is not None and t.shape != x_out.shape:
+            raise ValueError(f"{name} must have x_out's shape {tuple(x_out.shape)} (got {tuple(t.shape)})")
+    given = dx, dy
+    if dx is None:
+        dx = torch.empty_like(x_out, memory_format=torch.contiguous_format)
+    else:
+        _exactly(dx, "dx", x_out.dtype, dev, x_out.shape)
+    if y is None:
+        if dy is not None:
+            raise ValueError("dy without y")
+    elif dy is None:
+        dy = torch.empty_like(y, memory_format=torch.contiguous_format)
+    else:
+        _exactly(dy, "dy", y.dtype, dev, y.shape)
+    grads = [None if t is None else torch.empty_like(t, memory_format=torch.contiguous_format)
+             for t in (gate, residual_scale, post_weight, pre_weight)]
+    args = _resid_args(x_out, y, gate, residual_scale, post_weight, pre_weight, post, eps, p, seed, offset, dz.dtype,
+                       None, (dz, dx_out, x_out, x_in, dx, dy, *grads), dev)
+    if given[0] is not None or given[1] is not None:
+        reads = ((x_out, "x_out"), (x_in, "x"), (gate, "gate"), (residual_scale, "residual_scale"),
+                 (post_weight, "post_weight"), (pre_weight, "pre_weight"),
+                 (seed if isinstance(seed, torch.Tensor) else None, "seed"))
+        if given[0] is not None:
+            _apart(dx, "dx", (dx_out, "dx_out", True), (dz, "dz"), (y, "y"), *reads, (given[1], "dy"))
+        if given[1] is not None:
+            _apart(dy, "dy", (dx_out, "dx_out"), (dz, "dz", True), (y, "y", True), *reads)
+    ptr, size, ws = _ws(workspace, _lib.muon_residual_norm_backward_workspace_size(args) or 256, dev)
+    _call(dev, _lib.muon_residual_norm_backward, args, ptr, size)
+    return dx, dy, *grads
+
+
+def _matrix(t, name, dev, shape=None):
+    """bfloat16 rows on `dev`, one stride apart."""
+    _tensor(t, name, _BF16, dev, None if shape is None else len(shape))
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    return _rows(t, name)
+
+
+def _ffn_args(x, w_gate, w_up, w_down, activation, out, kept, dout, grads, dw_type, dev):
+    """The checked arguments as muon_feed_forward_args (None out, kept: none)."""
+    x_step = _matrix(x, "x", dev)
+    _tensor(w_gate, "w_gate", _BF16, dev, 2)
+    hidden, width = w_gate.shape
+    if x.shape[-1] != width:
+        raise ValueError(f"x {tuple(x.shape)} does not fit w_gate {tuple(w_gate.shape)}")
+    w_step = _matrix(w_gate, "w_gate", dev)
+    if _matrix(w_up, "w_up", dev, (hidden, width)) != w_step:
+        raise ValueError("the rows of w_gate and w_up must be the same stride apart")
+    down_step = _matrix(w_down, "w_down", dev, (width, hidden))
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)} (got {activation!r})")
+    tokens = x.numel() // width if width else 0
+    a = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    return _FFN.pack(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), a(out), a(kept), a(dout),
+                     *[a(t) for t in grads], x_step, w_step, down_step, 0 if dout is None else _rows(dout, "dout"),
+                     tokens, width, hidden, ACTIVATIONS[activation], _DTYPE[dw_type])
+
+
+def feed_forward(x, w_gate, w_up, w_down, activation="silu", keep=False, out=None, workspace=None):
+    """The gated feed-forward block of bfloat16 ``x`` (..., width):
+
+        (activation(x w_gate^T) * (x w_up^T)) w_down^T
+
+    with ``w_gate`` and ``w_up`` (hidden, width) and ``w_down`` (width, hidden),
+    bfloat16; returns a new (or given, contiguous) tensor of x's shape.
+    ``activation``: "silu", "gelu" (erf), "gelu_tanh" or "relu".  With ``keep``
+    it returns ``(out, kept)``: kept (3, tokens, hidden) holds what
+    ``feed_forward_backward`` needs, the gate, the up projection and their
+    product, rounded to bfloat16.
+
+    width and hidden are multiples of 8; rows are aligned to 16 bytes and one
+    stride (a multiple of 8) apart, the same for w_gate and w_up, so the halves
+    of one matrix serve.  Sums are float32; the hidden values are rounded once.
+    A given ``out`` must not share memory with anything."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    _tensor(x, "x", _BF16, dev)
+    if x.dim() == 0:
+        raise ValueError("x must have a last dimension")
+    given = out
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _exactly(out, "out", _BF16, dev, x.shape)
+    kept = None
+    if keep:
+        _tensor(w_gate, "w_gate", _BF16, dev, 2)
+        kept = torch.empty((3, x.numel() // x.shape[-1] if x.shape[-1] else 0, w_gate.shape[0]), dtype=_BF16, device=dev)
+    args = _ffn_args(x, w_gate, w_up, w_down, activation, out, kept, None, (None,) * 4, _BF16, dev)
+    if given is not None:
+        _apart(out, "out", (x, "x"), (w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))
+    ptr, size, ws = _ws(workspace, _lib.muon_feed_forward_workspace_size(args) or 256, dev)
+    _call(dev, _lib.muon_feed_forward, args, ptr, size)
+    return (out, kept) if keep else out
+
+
+def feed_forward_backward(dout, x, w_gate, w_up, w_down, kept, activation="silu", dtype=_BF16, dx=None,
+                          workspace=None):
+    """Gradients ``(dx, dw_gate, dw_up, dw_down)`` of ``feed_forward`` from
+    ``dout``, its arguments and what it kept.  dx is bfloat16; the matrices'
+    gradients are contiguous and of ``dtype`` (bfloat16, or float32: their sums
+    as they are).  The gradients of the gate and of the up projection are
+    rounded to bfloat16 once on the way.  A given ``dx`` must not share memory
+    with anything."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    _tensor(x, "x", _BF16, dev)
+    _matrix(dout, "dout", dev, x.shape)
+    _float_type(dtype, "dtype")
+    for t, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
+        _tensor(t, name, _BF16, dev, 2)
+    width, hidden = x.shape[-1] if x.dim() else 0, w_gate.shape[0]
+    _exactly(kept, "kept", _BF16, dev, (3, x.numel() // width if width else 0, hidden))
+    given = dx
+    if dx is None:
+        dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+    else:
+        _exactly(dx, "dx", _BF16, dev, x.shape)
+    dws = [torch.empty(w.shape, dtype=dtype, device=dev) for w in (w_gate, w_up, w_down)]
+    args = _ffn_args(x, w_gate, w_up, w_down, activation, None, kept, dout, (dx, *dws), dtype, dev)
+    if given is not None:
+        _apart(dx, "dx", (dout, "dout"), (x, "x"), (w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"),
+               (kept, "kept"))
+    ptr, size, ws = _ws(workspace, _lib.muon_feed_forward_backward_workspace_size(args) or 256, dev)
+    _call(dev, _lib.muon_feed_forward_backward, args, ptr, size)
+    return dx, *dws
