@@ -55,20 +55,16 @@ struct ResidPlan {
 };
 
 // Waves that hold a row: 1 up to 1024 values, then as many as keep it at two
-// pieces of 8 a lane (single values: at most 16 a lane).
+// pieces of 8 a lane.
 //
-// Backward, a workgroup leaves a row of sums, which are written and read again:
-// 4 workgroups a CU are enough to fill the memory's queues.
-ResidPlan plan_resid(const muon_residual_norm_args* x, bool vector, bool backward) {
+// Backward, a workgroup leaves a row of up to 4 sums, which are written and read
+// again (as much as two rows of data): at most as many workgroups as the chip
+// holds, and 4 turns of rows each.
+ResidPlan plan_resid(const muon_residual_norm_args* x, bool backward) {
     ResidPlan p{};
-    p.pieces = 2;
-    if (vector) {
-        const int64_t n = x->width / 8;
-        p.waves = n <= 128 ? 1 : n <= 256 ? 2 : n <= 512 ? 4 : 8;
-        if (n <= 64) p.pieces = 1;
-    } else {
-        p.waves = x->width <= 256 ? 1 : x->width <= 2048 ? 4 : 8;
-    }
+    const int64_t pieces = div_up(x->width, 8);
+    p.waves = pieces <= 128 ? 1 : pieces <= 256 ? 2 : pieces <= 512 ? 4 : 8;
+    p.pieces = pieces <= 64 ? 1 : 2;
     const int64_t rows = x->batch * x->s, per_block = p.waves >= 4 ? 1 : 4 / p.waves;
     p.chunks = p.per = 1;
     p.groups = 1;
@@ -78,10 +74,10 @@ ResidPlan plan_resid(const muon_residual_norm_args* x, bool vector, bool backwar
         p.bytes = 256;
         return p;
     }
-    const int64_t most = p.waves == 8 ? 512 : 1024;
+    const int64_t most = p.waves == 8 ? 256 : 512;
     const bool by_sequence = x->gate_kind == GATE_SEQUENCE;
     p.groups = by_sequence ? x->batch : 1;
-    const int64_t n = div_up(by_sequence ? x->s : rows, per_block);
+    const int64_t n = div_up(by_sequence ? x->s : rows, 4 * per_block);
     if (p.groups >= most) {
         p.per = static_cast<int>(div_up(p.groups, most));
         p.blocks = div_up(p.groups, p.per);
@@ -148,7 +144,7 @@ int run_resid(const muon_residual_norm_args* x, bool backward, void* ws, size_t 
     if (backward)
         if (int st = check_workspace(ws, ws_bytes, muon_residual_norm_backward_workspace_size(x))) return st;
     if (!backward && rows == 0) return done();
-    const ResidPlan p = plan_resid(x, vec, backward);
+    const ResidPlan p = plan_resid(x, backward);
     auto step = [&](int64_t stride) { return rows > 1 ? stride : 0; };
     a.x = x->x;
     a.y = block ? x->y : nullptr;
@@ -342,13 +338,7 @@ int muon_dropout(const void* x, void* out, int64_t n, int dtype, double p, uint6
 size_t muon_residual_norm_backward_workspace_size(const muon_residual_norm_args* x) {
     using namespace muon;
     if (check_resid(x)) return 0;
-    // the pointers' alignment, which decides between the two plans, is not looked at here
-    size_t n = 256;
-    for (const bool vector : {false, true}) {
-        const size_t bytes = plan_resid(x, vector, true).bytes;
-        if (bytes > n) n = bytes;
-    }
-    return n;
+    return plan_resid(x, true).bytes;
 }
 
 int muon_residual_norm(const muon_residual_norm_args* x, void* stream) {
