@@ -16,7 +16,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["api.hip", "momentum.hip", "norm_cast.hip", "gemm.hip", "f32_iter.hip", "static_ws.hip", "polar_svd.hip",
            "small.hip", "lm_api.hip", "attn_fwd.hip", "attn_bwd.hip", "qk_norm.hip", "embed.hip", "layer_api.hip",
-           "ffn.hip", "resid_norm.hip", "dropout.hip"]
+           "ffn.hip", "ffn_few.hip", "resid_norm.hip", "dropout.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # packed-fp32 instructions are kept out of the generated code

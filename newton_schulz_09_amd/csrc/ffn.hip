@@ -18,8 +18,7 @@
 // The matrix instruction takes Q first, so a lane holds 4 consecutive columns
 // of one output row; two lanes swap halves and each stores 16 bytes.
 #include "../../include/muon.h"
-#include "attn_common.hpp"
-#include "layer_common.hpp"
+#include "ffn_common.hpp"
 
 namespace muon {
 
@@ -32,12 +31,9 @@ using attn::landed;
 using attn::lane_id;
 using attn::lds_addr;
 using attn::load_lds16;
-using attn::mfma;
 using attn::s16x4;
-using attn::u32x2;
-using attn::u32x4;
+using namespace ffn;
 
-constexpr int kBk = 64;      // K values of a step
 constexpr int kXcds = 8;
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer's end
 
@@ -48,9 +44,13 @@ __device__ __forceinline__ int xcd_place(int b, int n) {
     return x * q + (x < r ? x : r) + b / kXcds;
 }
 
-// Slot of 16-byte chunk c of row r is c ^ f(r).  Rows of K (8 chunks): 16 rows
-// of one chunk fall on distinct banks.
-__device__ __forceinline__ int rows_swizzle(int r) { return ((r >> 1) ^ (r << 2)) & 7; }
+// Slot of 16-byte chunk c of row r is c ^ f(r).  Rows of K (8 or 4 chunks): 16
+// rows of one chunk fall on distinct banks.
+template <int CPR>
+__device__ __forceinline__ int rows_swizzle(int r) {
+    if constexpr (CPR == 8) return ((r >> 1) ^ (r << 2)) & 7;
+    else return ((r >> 1) ^ (r >> 3)) & 3;
+}
 // Rows of output (CPR chunks): the 8 rows that a transposing read touches (two
 // runs of 4, 8 apart) fall on distinct banks.
 template <int CPR>
@@ -58,15 +58,15 @@ __device__ __forceinline__ int columns_swizzle(int r) {
     return ((((r & 3) << 1) | ((r >> 3) & 1)) * (CPR >= 16 ? 2 : 1)) & (CPR - 1);
 }
 
-// One operand's tile: B output rows (or columns) by kBk of K, COL: contiguous
+// One operand's tile: B output rows (or columns) by BK of K, COL: contiguous
 // along the output.  NW waves load it, N loads of 1 KB a wave.
-template <int B, bool COL, int NW>
+template <int B, int BK, bool COL, int NW>
 struct Operand {
-    static constexpr int CPR = COL ? B / 8 : kBk / 8;
+    static constexpr int CPR = COL ? B / 8 : BK / 8;
     static constexpr int RPI = 64 / CPR;  // rows per load
-    static constexpr int LROWS = COL ? kBk : B;
+    static constexpr int LROWS = COL ? BK : B;
     static constexpr int N = LROWS / RPI / NW;
-    static constexpr int BYTES = B * kBk * 2;
+    static constexpr int BYTES = B * BK * 2;
     static_assert(N * RPI * NW == LROWS, "whole loads per wave");
     uint32_t voff[N];
     uint64_t base;     // of the tile, at K = 0
@@ -76,7 +76,7 @@ struct Operand {
 
     __device__ __forceinline__ static int row_of(int wave, int i) { return (wave * N + i) * RPI + lane_id() / CPR; }
     __device__ __forceinline__ static int chunk_of(int row) {
-        return (lane_id() % CPR) ^ (COL ? columns_swizzle<CPR>(row) : rows_swizzle(row));
+        return (lane_id() % CPR) ^ (COL ? columns_swizzle<CPR>(row) : rows_swizzle<CPR>(row));
     }
     // first: the tile's first output row; n: their number; place(row): the row's place from `first` on
     template <typename F>
@@ -95,8 +95,8 @@ struct Operand {
     // Lets through the first `lim` K values of a step (rows of K).
     __device__ __forceinline__ void limit(int64_t lim, int wave) {
         if constexpr (!COL) {
-            if (lim >= kBk && !masked) return;
-            masked = lim < kBk;
+            if (lim >= BK && !masked) return;
+            masked = lim < BK;
 #pragma unroll
             for (int i = 0; i < N; ++i)
                 voff[i] = 8 * chunk_of(row_of(wave, i)) >= lim ? voff[i] | kOut : voff[i] & ~kOut;
@@ -105,117 +105,75 @@ struct Operand {
     // Descriptor of the step from K = k0 on, lim = K - k0 > 0; rows: output rows of the tile
     __device__ __forceinline__ u32x4 step(uint64_t at, int64_t k0, int64_t lim, int rows) const {
         if constexpr (COL) {
-            const uint32_t n = static_cast<uint32_t>(lim < kBk ? lim : kBk);
+            const uint32_t n = static_cast<uint32_t>(lim < BK ? lim : BK);
             return descriptor(reinterpret_cast<const void*>(at + k0 * ld2),
                               (n - 1) * ld2 + 2 * static_cast<uint32_t>(left < B ? left : B));
         } else {
             const uint32_t n = static_cast<uint32_t>(left < rows ? left : rows);
             return descriptor(reinterpret_cast<const void*>(at + 2 * k0),
-                              (n - 1) * ld2 + 2 * static_cast<uint32_t>(lim < kBk ? lim : kBk));
+                              (n - 1) * ld2 + 2 * static_cast<uint32_t>(lim < BK ? lim : BK));
         }
+    }
+    // The next step's, where that is a whole one of the same product.
+    __device__ __forceinline__ void advance(u32x4& d) const {
+        const uint64_t at = (static_cast<uint64_t>(d.y) << 32 | d.x) + (COL ? static_cast<uint64_t>(BK) * ld2 : 2 * BK);
+        d.x = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(at)));
+        d.y = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(at >> 32)));
     }
     __device__ __forceinline__ void load(int i, uint32_t lds, int wave, u32x4 desc) const {
         load_lds16(lds + (wave * N + i) * 1024, voff[i], desc);
     }
 };
 
-// Fragments of 32 output rows from `row0` on, for the 16 K values of slice kk:
-// lane l holds row l % 32, K 8 (l / 32) .. + 7.
-template <int B, bool COL, int NF>
+// Fragments of 16 output rows, f of them from `row0` on, for the 32 K values of
+// slice kk: lane l holds row l % 16, K 8 (l / 16) .. + 7.
+template <int B, int BK, bool COL>
 struct Frags {
-    uint32_t off[COL ? NF : kBk / 16];
+    uint32_t off;
     __device__ __forceinline__ void init(int row0) {
-        const int l = lane_id();
+        const int l = lane_id(), g = l >> 4, r = l & 15;
         if constexpr (COL) {
-            const int g = l >> 4, r = l & 15, row = 8 * (g >> 1) + (r >> 2);
-#pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                const int col = row0 + 32 * f + 16 * (g & 1) + 4 * (r & 3);
-                off[f] = 2 * (row * B + (((col >> 3) ^ columns_swizzle<B / 8>(row)) << 3) + (col & 7));
-            }
+            // transposing reads: lane r of 16 points at K r / 4 and 4 columns
+            const int row = 8 * g + (r >> 2), col = row0 + 4 * (r & 3);
+            off = 2 * (row * B + (((col >> 3) ^ columns_swizzle<B / 8>(row)) << 3) + (col & 7));
         } else {
-            const int r = l & 31, h = l >> 5;
-#pragma unroll
-            for (int kk = 0; kk < kBk / 16; ++kk) off[kk] = 2 * ((row0 + r) * kBk + (((2 * kk + h) ^ rows_swizzle(r)) << 3));
+            off = 2 * ((row0 + r) * BK + ((g ^ rows_swizzle<BK / 8>(r)) << 3));
         }
     }
-    __device__ __forceinline__ bf16x8 read(uint32_t tile, int kk, int f) const {
+    // (the fragment's number, and of rows of K the slice's, are bits of the
+    // chunk apart from those of row0: they go in by exclusive or, as the swizzle does)
+    template <int KK, int F>
+    __device__ __forceinline__ bf16x8 read(uint32_t tile) const {
         if constexpr (COL) {
-            const uint32_t at = tile + off[f] + 32 * kk * B;
+            const uint32_t at = ((tile + off) ^ (32 * F)) + 64 * KK * B;
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 8 * B));
             return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            return __builtin_bit_cast(bf16x8, *(__attribute__((address_space(3))) const u32x4*)(tile + off[kk] + 64 * f * kBk));
+            return __builtin_bit_cast(bf16x8, *(__attribute__((address_space(3))) const u32x4*)(((tile + off) ^ (64 * KK)) + 32 * F * BK));
         }
     }
 };
 
-constexpr float kLog2E = 1.4426950408889634f;
-__device__ __forceinline__ float sigmoid(float x) {
-    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2E * x));
-}
-// act(g), and its derivative.  The hardware's exponential and reciprocal are
-// good to an ulp, far below the bfloat16 that the results are rounded to.
-__device__ __forceinline__ float activate(int act, float g) {
-    if (act == ACT_SILU) return g * sigmoid(g);
-    if (act == ACT_GELU) return 0.5f * g * (1.0f + erff(g * 0.70710678118654752f));
-    // (1 + tanh v) / 2 = sigmoid(2 v)
-    if (act == ACT_GELU_TANH) return g * sigmoid(1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f));
-    return g < 0.0f ? 0.0f : g;
-}
-__device__ __forceinline__ void activate_both(int act, float g, float& a, float& da) {
-    if (act == ACT_SILU) {
-        const float s = sigmoid(g);
-        a = g * s;
-        da = fmaf(a, 1.0f - s, s);
-    } else if (act == ACT_GELU) {
-        const float c = 0.5f * (1.0f + erff(g * 0.70710678118654752f));
-        a = g * c;
-        da = fmaf(g * 0.3989422804014327f, __builtin_amdgcn_exp2f(-0.5f * kLog2E * g * g), c);
-    } else if (act == ACT_GELU_TANH) {
-        const float s = sigmoid(1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f));
-        a = g * s;
-        da = fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), s);
-    } else {
-        a = g < 0.0f ? 0.0f : g;
-        da = g > 0.0f ? 1.0f : 0.0f;
-    }
+// This wave's loads have landed but for the last N, and its LDS reads are done,
+// and so for every wave of the workgroup.
+template <int N>
+__device__ __forceinline__ void landed_but() {
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
-    return u32x4{f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]), f32x2_to_bf16x2(v[4], v[5]),
-                 f32x2_to_bf16x2(v[6], v[7])};
-}
-__device__ __forceinline__ void spread8(u32x4 u, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-// Results 8 t .. 8 t + 7 of a fragment as the 8 consecutive columns 16 t + 8
-// half .. + 7: the halves of the wave swap runs of 4.
-__device__ __forceinline__ void columns8(const f32x16& c, int t, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(c[8 * t + i]), __float_as_uint(c[8 * t + 4 + i]), false, false);
-        v[i] = __uint_as_float(r[0]);
-        v[4 + i] = __uint_as_float(r[1]);
-    }
-}
-
-template <int KIND, int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(const FfnGemm g) {
+template <int KIND, int BM, int BN, int WGM, int WGN, int BK>
+__global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 2) void k_ffn(const FfnGemm g) {
     constexpr bool PT = KIND == FFN_WEIGHTS, QT = KIND == FFN_HIDDEN || KIND == FFN_INPUT || KIND == FFN_WEIGHTS;
     constexpr bool GATED = KIND == FFN_GATED;
-    constexpr int NW = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 32, FN = WTN / 32;
-    static_assert(!GATED || FN % 2 == 0, "a wave holds the gate and up columns of the same h");
-    using P = Operand<BM, PT, NW>;
-    using Q = Operand<BN, QT, NW>;
-    static_assert(!GATED || 32 % (Q::N * Q::RPI) == 0, "a wave loads rows of one matrix");
-    constexpr int STAGE = P::BYTES + Q::BYTES;
-    __shared__ __attribute__((aligned(1024))) char lds_mem[2 * STAGE];
+    constexpr int NW = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 16, FN = WTN / 16;
+    static_assert(!GATED || FN % 4 == 0, "a wave holds the gate and up columns of the same h");
+    using P = Operand<BM, BK, PT, NW>;
+    using Q = Operand<BN, BK, QT, NW>;
+    static_assert(!GATED || 32 % Q::RPI == 0, "a load takes rows of one matrix");
+    constexpr int STRIP = 32 * WTN * 4, QAT = 3 * P::BYTES, LDS = QAT + 2 * Q::BYTES;
+    static_assert(NW * STRIP <= LDS, "the results pass through the stages' memory");
+    __shared__ __attribute__((aligned(1024))) char lds_mem[LDS];
     const uint32_t lds = lds_addr(lds_mem);
 
     // ---- which split, segment and tile
@@ -239,162 +197,258 @@ __global__ __launch_bounds__(64 * WGM * WGN) void k_ffn(const FfnGemm g) {
     P p;
     Q q;
     p.init(seg.p[0], seg.ldp, i0, seg.m, wave, [](int r) { return r; });
-    const bool up_rows = GATED && (wave * Q::N * Q::RPI / 32) & 1;
-    q.init(up_rows ? seg.q[1] : seg.q[0], seg.ldq, j0, seg.n, wave,
+    q.init(seg.q[0], seg.ldq, j0, seg.n, wave,
            [](int r) { return GATED ? r / 64 * 32 + r % 32 : r; });
     const uint64_t p_next = KIND == FFN_INPUT ? p.base + (reinterpret_cast<uint64_t>(seg.p[1]) - reinterpret_cast<uint64_t>(seg.p[0])) : p.base;
-    const uint64_t q_next = KIND == FFN_INPUT ? q.base + (reinterpret_cast<uint64_t>(seg.q[1]) - reinterpret_cast<uint64_t>(seg.q[0])) : q.base;
+    const uint64_t q_next = KIND == FFN_INPUT || GATED ? q.base + (reinterpret_cast<uint64_t>(seg.q[1]) - reinterpret_cast<uint64_t>(seg.q[0])) : q.base;
 
-    const int phase_steps = static_cast<int>((g.k + kBk - 1) / kBk), steps = phase_steps * g.phases;
+    const int phase_steps = static_cast<int>((g.k + BK - 1) / BK), steps = phase_steps * g.phases;
     const int s0 = split * g.split_steps, s1 = s0 + g.split_steps < steps ? s0 + g.split_steps : steps;
-    u32x4 dp, dq;
-    auto aim = [&](int s) {  // the loads of step s
-        const bool second = KIND == FFN_INPUT && s >= phase_steps;
-        const int64_t k0 = static_cast<int64_t>(second ? s - phase_steps : s) * kBk, lim = g.k - k0;
-        p.limit(lim, wave);
-        q.limit(lim, wave);
-        dp = p.step(second ? p_next : p.base, k0, lim, BM);
-        dq = q.step(second ? q_next : q.base, k0, lim, BNO);
+    u32x4 dp, dq, dq_up;
+    // Aims the loads at step s, the one after the step they were aimed at.  Most
+    // steps move the descriptors on; the first and last ones of a product make
+    // them anew (made anew at every step they cost a tenth of the loop's time).
+    auto plain = [&](int s) {
+        return s > s0 && s != phase_steps - 1 && (KIND != FFN_INPUT || (s != phase_steps && s != 2 * phase_steps - 1));
     };
-    auto load = [&](int L, uint32_t stage) {
-        if (L < P::N) p.load(L, stage, wave, dp);
-        else q.load(L - P::N, stage + P::BYTES, wave, dq);
+    auto place_of = [&](int s, bool& second, int64_t& k0) {
+        second = KIND == FFN_INPUT && s >= phase_steps;
+        k0 = static_cast<int64_t>(second ? s - phase_steps : s) * BK;
     };
-    Frags<BM, PT, FM> fp;
-    Frags<BN, QT, FN> fq;
+    auto aim_p = [&](int s) {
+        if (plain(s)) return p.advance(dp);
+        bool second;
+        int64_t k0;
+        place_of(s, second, k0);
+        p.limit(g.k - k0, wave);
+        dp = p.step(second ? p_next : p.base, k0, g.k - k0, BM);
+    };
+    auto aim_q = [&](int s) {
+        if (plain(s)) {
+            if constexpr (GATED) q.advance(dq_up);
+            return q.advance(dq);
+        }
+        bool second;
+        int64_t k0;
+        place_of(s, second, k0);
+        q.limit(g.k - k0, wave);
+        dq = q.step(second ? q_next : q.base, k0, g.k - k0, BNO);
+        if constexpr (GATED) dq_up = q.step(q_next, k0, g.k - k0, BNO);
+    };
+    auto load_p = [&](int i, uint32_t to) { p.load(i, to, wave, dp); };
+    auto load_q = [&](int i, uint32_t to) { q.load(i, to, wave, GATED && ((wave * Q::N + i) * Q::RPI / 32) & 1 ? dq_up : dq); };
+    Frags<BM, BK, PT> fp;
+    Frags<BN, BK, QT> fq;
     fp.init(wm * WTM);
     fq.init(wn * WTN);
 
-    f32x16 acc[FM][FN];
-#pragma unroll
-    for (int m = 0; m < FM; ++m)
-#pragma unroll
-        for (int n = 0; n < FN; ++n) acc[m][n] = attn::splat(0.0f);
+    // A step is two slices of 32 K.  The operand of which a wave holds more
+    // fragments is the outer one: each of its fragments meets all of the inner
+    // operand's, and is then replaced by its successor of the next slice, so the
+    // outer operand is held once and the inner twice.
+    constexpr bool P_OUTER = FM >= FN;
+    constexpr int NO = P_OUTER ? FM : FN, NI = P_OUTER ? FN : FM;
+    f32x4 acc[NO][NI];
+    each<0, NO>([&](auto o) { each<0, NI>([&](auto i) { acc[o][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f}; }); });
+    bf16x8 outer[NO], inner[2][NI];
+    auto read_outer = [&](auto kk, auto f, uint32_t p_tile, uint32_t q_tile) {
+        if constexpr (P_OUTER) outer[f] = fp.template read<kk, f>(p_tile);
+        else outer[f] = fq.template read<kk, f>(q_tile);
+    };
+    auto read_inner = [&](auto kk, auto f, uint32_t p_tile, uint32_t q_tile) {
+        if constexpr (P_OUTER) inner[kk][f] = fq.template read<kk, f>(q_tile);
+        else inner[kk][f] = fp.template read<kk, f>(p_tile);
+    };
 
-    constexpr int NL = P::N + Q::N, NKK = kBk / 16, NMF = FM * FN, NR = FM + FN, TOT = NKK * NMF;
-    constexpr int RWIN = NMF * 3 / 4 > 0 ? NMF * 3 / 4 : 1, LWIN = TOT / 2;
+    // The barrier lies behind a quarter of the second slice, when the next step
+    // has landed and every wave has read all of this one: the products before it
+    // cover the last reads of this step, those behind it the first reads of the
+    // next.  Loads are spread over the products (in a burst they fill the memory
+    // pipe's queue, and the products behind them wait): those of P, which has
+    // three stages, two steps early in the first slice, those of Q one step early
+    // behind the barrier.
+    constexpr int WAIT = NO / 4;  // groups of the second slice in front of the barrier
+    static_assert(BK == 64 && NO >= 4, "two slices, four groups");
+    constexpr std::integral_constant<int, 0> first{};
+    constexpr std::integral_constant<int, 1> second{};
     if (s0 < s1) {
-        aim(s0);
-#pragma unroll
-        for (int L = 0; L < NL; ++L) load(L, lds);
+        aim_p(s0);
+        each<0, P::N>([&](auto i) { load_p(i, lds); });
+        aim_q(s0);
+        each<0, Q::N>([&](auto i) { load_q(i, lds + QAT); });
+        if (s0 + 1 < s1) {
+            aim_p(s0 + 1);
+            each<0, P::N>([&](auto i) { load_p(i, lds + P::BYTES); });
+            aim_q(s0 + 1);
+            each<0, Q::N>([&](auto i) { load_q(i, lds + QAT + Q::BYTES); });
+            landed_but<P::N + Q::N>();
+        } else {
+            landed();
+        }
+        each<0, NI>([&](auto i) { read_inner(first, i, lds, lds + QAT); });
+        each<0, NO>([&](auto o) { read_outer(first, o, lds, lds + QAT); });
     }
+    uint32_t p_here = lds, p_there = lds + P::BYTES, p_third = lds + 2 * P::BYTES;
+    uint32_t q_here = lds + QAT, q_there = lds + QAT + Q::BYTES;
     for (int s = s0; s < s1; ++s) {
-        landed();
-        const uint32_t here = lds + ((s - s0) & 1) * STAGE, there = lds + ((s - s0 + 1) & 1) * STAGE;
-        const bool more = s + 1 < s1;
-        if (more) aim(s + 1);
-        bf16x8 a[2][FM], b[2][FN];
-#pragma unroll
-        for (int m = 0; m < FM; ++m) a[0][m] = fp.read(here, 0, m);
-#pragma unroll
-        for (int n = 0; n < FN; ++n) b[0][n] = fq.read(here + P::BYTES, 0, n);
-        // products of slice kk, with the reads of slice kk + 1 and the next
-        // step's loads between them in this order
-#pragma unroll
-        for (int kk = 0; kk < NKK; ++kk) {
-            const int c = kk & 1, o = c ^ 1;
-#pragma unroll
-            for (int i = 0; i < NMF; ++i) {
-                in_order();
-                acc[i / FN][i % FN] = mfma(b[c][i % FN], a[c][i / FN], acc[i / FN][i % FN]);
-                in_order();
-                if (kk + 1 < NKK) {
-#pragma unroll
-                    for (int r = 0; r < NR; ++r)
-                        if (r * RWIN / NR == i) {
-                            if (r < FM) a[o][r] = fp.read(here, kk + 1, r);
-                            else b[o][r - FM] = fq.read(here + P::BYTES, kk + 1, r - FM);
-                        }
+        const bool more = s + 1 < s1, more2 = s + 2 < s1;
+        in_order();
+        if (more2) aim_p(s + 2);
+        each<0, 2>([&](auto kk) {
+            each<0, NO>([&](auto o) {
+                if constexpr (kk == 1 && o == WAIT) {
+                    in_order();
+                    if (more2) {
+                        landed_but<P::N>();  // (P of two steps on is under way)
+                        aim_q(s + 2);
+                    } else {
+                        landed();
+                    }
+                    if (more) each<0, WAIT>([&](auto f) { read_outer(first, f, p_there, q_there); });
                 }
-                if (more) {
+                each<0, NI>([&](auto i) {
+                    in_order();
+                    if constexpr (P_OUTER) acc[o][i] = mfma16(inner[kk][i], outer[o], acc[o][i]);
+                    else acc[o][i] = mfma16(outer[o], inner[kk][i], acc[o][i]);
+                });
+                in_order();
+                // the next slice's fragments
+                if constexpr (kk == 0) {
+                    read_outer(second, o, p_here, q_here);
+                    each<0, NI>([&](auto i) {
+                        if constexpr (i * NO / NI == o) read_inner(second, i, p_here, q_here);
+                    });
+                    if (more2)
+                        each<0, P::N>([&](auto L) {
+                            if constexpr (L * NO / P::N == o) load_p(L, p_third);
+                        });
+                } else if constexpr (o >= WAIT) {
+                    if (more) {
+                        read_outer(first, o, p_there, q_there);
+                        each<0, NI>([&](auto i) {
+                            if constexpr (WAIT + i * (NO - WAIT) / NI == o) read_inner(first, i, p_there, q_there);
+                        });
+                    }
+                    if (more2)
+                        each<0, Q::N>([&](auto L) {
+                            if constexpr (WAIT + L * (NO - WAIT) / Q::N == o) load_q(L, q_here);
+                        });
+                }
+            });
+        });
+        in_order();
+        const uint32_t free = p_here;
+        p_here = p_there;
+        p_there = p_third;
+        p_third = free;
+        const uint32_t other = q_here;
+        q_here = q_there;
+        q_there = other;
+    }
+
+    // ---- results.  Lane l holds row l % 16 of a fragment, the 4 columns 4 (l / 16)
+    // .. + 3.  Strips of 32 rows pass through LDS in float32, 16-byte chunk c
+    // of row r at slot c ^ r, so that memory is read and written in whole rows of
+    // a wave's columns, 8 columns a lane.
+    constexpr int CH = WTN / 4, COLS = GATED ? WTN / 2 : WTN, LPR = COLS / 8, RPS = 64 / LPR;  // lanes a row, rows a turn
+    const uint32_t strip = lds + wave * STRIP;
+    const int64_t row0 = i0 + wm * WTM, col = j0 + wn * COLS + 8 * (lane % LPR);
+    typedef __attribute__((address_space(3))) f32x4* Chunk;
+    float* part = nullptr;
+    if constexpr (KIND >= FFN_INPUT || KIND == FFN_PLAIN)
+        part = seg.part ? seg.part + static_cast<int64_t>(split) * seg.m * seg.n : nullptr;
+    constexpr int TURNS = 32 / RPS;
+    u32x4 gates[2][KIND == FFN_HIDDEN ? TURNS : 1][2];  // gate and up of this strip and the next, under way
+    auto fetch = [&](auto m) {
+        if constexpr (KIND == FFN_HIDDEN && m < WTM / 32)
+            each<0, TURNS>([&](auto k) {
+                int64_t row = row0 + 32 * m + k * RPS + lane / LPR;
+                if (row >= seg.m) row = seg.m - 1;
+                const int64_t at = row * seg.n + (col < seg.n ? col : 0);
+                gates[m & 1][k][0] = *reinterpret_cast<const u32x4*>(g.gate + at);
+                gates[m & 1][k][1] = *reinterpret_cast<const u32x4*>(g.up + at);
+            });
+    };
+    fetch(first);
+    // every wave has read its last fragments (no load to LDS is under way)
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    each<0, WTM / 32>([&](auto m) {
+        fetch(std::integral_constant<int, m + 1>{});
+        each<0, 2>([&](auto h) {
+            each<0, FN>([&](auto n) {
+                constexpr int o = P_OUTER ? 2 * m + h : n, i = P_OUTER ? n : 2 * m + h;
+                const int r = 16 * h + (lane & 15), c = 4 * n + (lane >> 4);
+                *(Chunk)(strip + r * WTN * 4 + ((c ^ r) & (CH - 1)) * 16) = acc[o][i];
+            });
+        });
+        each<0, TURNS>([&](auto k) {
+            const int r = k * RPS + lane / LPR;
+            const int64_t row = row0 + 32 * m + r;
+            auto take = [&](int c, float (&v)[8]) {  // chunks c and c + 1 of the row
+                const f32x4 lo = *(Chunk)(strip + r * WTN * 4 + ((c ^ r) & (CH - 1)) * 16);
+                const f32x4 hi = *(Chunk)(strip + r * WTN * 4 + (((c + 1) ^ r) & (CH - 1)) * 16);
 #pragma unroll
-                    for (int L = 0; L < NL; ++L)
-                        if (L * LWIN / NL == kk * NMF + i) load(L, there);
+                for (int i = 0; i < 4; ++i) {
+                    v[i] = lo[i];
+                    v[4 + i] = hi[i];
+                }
+            };
+            const int64_t at = row * seg.n + col;
+            const bool in = row < seg.m && col < seg.n;
+            if constexpr (GATED) {
+                // 32 columns of the gate, then the same 32 of the up projection
+                const int q8 = lane % LPR, c = q8 / 4 * 16 + q8 % 4 * 2;
+                float gt[8], up[8], h[8];
+                take(c, gt);
+                take(c + 8, up);
+                by_act(g.act, [&](auto act) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float v, unused;
+                        activate<act>(gt[i], v, unused);
+                        h[i] = v * up[i];
+                    }
+                });
+                if (in) {
+                    *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(h);
+                    if (g.gate) {
+                        *reinterpret_cast<u32x4*>(g.gate + at) = pack8(gt);
+                        *reinterpret_cast<u32x4*>(g.up + at) = pack8(up);
+                    }
+                }
+            } else if constexpr (KIND == FFN_HIDDEN) {
+                float dh[8], gt[8], up[8];
+                take(2 * (lane % LPR), dh);
+                spread8(gates[m & 1][k][0], gt);
+                spread8(gates[m & 1][k][1], up);
+                by_act(g.act, [&](auto act) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float v, dv;
+                        activate<act>(gt[i], v, dv);
+                        gt[i] = dh[i] * up[i] * dv;
+                        up[i] = dh[i] * v;
+                    }
+                });
+                if (in) {
+                    *reinterpret_cast<u32x4*>(g.dgate + at) = pack8(gt);
+                    *reinterpret_cast<u32x4*>(g.dup + at) = pack8(up);
+                }
+            } else {
+                float v[8];
+                take(2 * (lane % LPR), v);
+                if (in) {
+                    if (part || g.out_f32) {
+                        float* o = (part ? part : static_cast<float*>(seg.out)) + at;
+                        reinterpret_cast<f32x4*>(o)[0] = f32x4{v[0], v[1], v[2], v[3]};
+                        reinterpret_cast<f32x4*>(o)[1] = f32x4{v[4], v[5], v[6], v[7]};
+                    } else {
+                        *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(v);
+                    }
                 }
             }
-        }
-        in_order();
-    }
-
-    // ---- results: lane l holds row l % 32 of a fragment
-    const int half = lane >> 5;
-    const int64_t row0 = i0 + wm * WTM + (lane & 31);
-    if constexpr (GATED) {
-#pragma unroll
-        for (int m = 0; m < FM; ++m) {
-            const int64_t row = row0 + 32 * m;
-#pragma unroll
-            for (int n = 0; n < FN / 2; ++n)
-#pragma unroll
-                for (int t8 = 0; t8 < 2; ++t8) {
-                    const int64_t col = j0 + wn * (WTN / 2) + 32 * n + 16 * t8 + 8 * half;
-                    float gt[8], up[8], h[8];
-                    columns8(acc[m][2 * n], t8, gt);
-                    columns8(acc[m][2 * n + 1], t8, up);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = activate(g.act, gt[i]) * up[i];
-                    if (row < seg.m && col < seg.n) {
-                        const int64_t at = row * seg.n + col;
-                        *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(h);
-                        if (g.gate) {
-                            *reinterpret_cast<u32x4*>(g.gate + at) = pack8(gt);
-                            *reinterpret_cast<u32x4*>(g.up + at) = pack8(up);
-                        }
-                    }
-                }
-        }
-    } else if constexpr (KIND == FFN_HIDDEN) {
-#pragma unroll
-        for (int m = 0; m < FM; ++m) {
-            const int64_t row = row0 + 32 * m;
-#pragma unroll
-            for (int n = 0; n < FN; ++n)
-#pragma unroll
-                for (int t8 = 0; t8 < 2; ++t8) {
-                    const int64_t col = j0 + wn * WTN + 32 * n + 16 * t8 + 8 * half;
-                    float dh[8], gt[8], up[8];
-                    columns8(acc[m][n], t8, dh);
-                    if (row < seg.m && col < seg.n) {
-                        const int64_t at = row * seg.n + col;
-                        spread8(*reinterpret_cast<const u32x4*>(g.gate + at), gt);
-                        spread8(*reinterpret_cast<const u32x4*>(g.up + at), up);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float v, dv;
-                            activate_both(g.act, gt[i], v, dv);
-                            gt[i] = dh[i] * up[i] * dv;
-                            up[i] = dh[i] * v;
-                        }
-                        *reinterpret_cast<u32x4*>(g.dgate + at) = pack8(gt);
-                        *reinterpret_cast<u32x4*>(g.dup + at) = pack8(up);
-                    }
-                }
-        }
-    } else {
-        float* part = seg.part ? seg.part + static_cast<int64_t>(split) * seg.m * seg.n : nullptr;
-#pragma unroll
-        for (int m = 0; m < FM; ++m) {
-            const int64_t row = row0 + 32 * m;
-#pragma unroll
-            for (int n = 0; n < FN; ++n)
-#pragma unroll
-                for (int t8 = 0; t8 < 2; ++t8) {
-                    const int64_t col = j0 + wn * WTN + 32 * n + 16 * t8 + 8 * half;
-                    float v[8];
-                    columns8(acc[m][n], t8, v);
-                    if (row < seg.m && col < seg.n) {
-                        const int64_t at = row * seg.n + col;
-                        if (part || g.out_f32) {
-                            float* o = (part ? part : static_cast<float*>(seg.out)) + at;
-                            reinterpret_cast<f32x4*>(o)[0] = f32x4{v[0], v[1], v[2], v[3]};
-                            reinterpret_cast<f32x4*>(o)[1] = f32x4{v[4], v[5], v[6], v[7]};
-                        } else {
-                            *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(v);
-                        }
-                    }
-                }
-        }
-    }
+        });
+    });
 }
 
 // Sums of the splits, in their order: 8 values a thread.
@@ -422,15 +476,19 @@ __global__ __launch_bounds__(256) void k_ffn_join(const FfnGemm g) {
 }
 
 template <int KIND>
-void start(int tile, const FfnGemm& g, hipStream_t stream) {
+void start(FfnTile tile, const FfnGemm& g, hipStream_t stream) {
     const uint32_t blocks = static_cast<uint32_t>(g.tiles) * g.splits;
-    if (tile == 256) k_ffn<KIND, 256, 256, 2, 4><<<blocks, 512, 0, stream>>>(g);
-    else k_ffn<KIND, 128, 128, 2, 2><<<blocks, 256, 0, stream>>>(g);
+    // The gated product's waves hold 64 rows by 128 columns, so that each writes
+    // rows of 64 hidden values; the others' 128 by 64.  (GPT-2 124M batch: gated
+    // 500 us against 540, gradients of the matrices 565 us and 552.)
+    constexpr int WGM = KIND == FFN_GATED ? 4 : 2;
+    if (tile == FFN_256) k_ffn<KIND, 256, 256, WGM, 8 / WGM, 64><<<blocks, 512, 0, stream>>>(g);
+    else k_ffn<KIND, 128, 128, 2, 2, 64><<<blocks, 256, 0, stream>>>(g);
 }
 
 }  // namespace
 
-hipError_t launch_ffn(FfnKind kind, int tile, const FfnGemm& g, hipStream_t stream) {
+hipError_t launch_ffn(FfnKind kind, FfnTile tile, const FfnGemm& g, hipStream_t stream) {
     switch (kind) {
         case FFN_GATED: start<FFN_GATED>(tile, g, stream); break;
         case FFN_PLAIN: start<FFN_PLAIN>(tile, g, stream); break;

@@ -229,23 +229,33 @@ int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, in
 }
 
 struct FfnPlan {
-    int tile, splits;
+    FfnTile tile;
+    int splits;
 };
 
 // The tile and the number of splits of K that take the least time: rounds of
 // workgroups over the CUs times the steps of one, and the sums of the splits.
-FfnPlan plan_ffn(int64_t m, int64_t n, int64_t steps, int count, bool may_split) {
-    FfnPlan best{128, 1};
+// k: length of one product; phases: products summed.
+//
+// Measured on the products of a GPT-2 124M batch (65536 tokens, 768 to 2048), in
+// microseconds: a step of a 256 tile, one of which a CU holds, 1.9, of 128 tiles,
+// of which it holds two, 1.22; around the steps, where results are written, 8
+// and 4.5; where gate and up are read and their gradients written, 30 and 10.
+// (So the gradient of the hidden values takes 128 tiles, 396 us against 426, and
+// the others 256, gradients of the matrices 565 against 730.)
+FfnPlan plan_ffn(FfnKind kind, int64_t m, int64_t n, int64_t k, int phases, int count, bool may_split) {
+    FfnPlan best{FFN_128, 1};
     double least = 1e300;
-    for (const int tile : {256, 128}) {
-        const int64_t tiles = div_up(m, tile) * div_up(n, tile) * count, slots = tile == 256 ? 256 : 512;
-        // microseconds: a step of all workgroups that a CU holds, and what a
-        // workgroup spends before and after its steps
-        const double step = tile == 256 ? 1.8 : 1.0, over = tile == 256 ? 6.0 : 4.0;
+    const int64_t steps = div_up(k, kFfnStep) * phases;
+    for (const FfnTile tile : {FFN_256, FFN_128}) {
+        const bool big = tile == FFN_256;
+        const int64_t tiles = div_up(m, tile) * div_up(n, tile) * count, slots = big ? 256 : 512;
+        const double step = big ? 1.9 : 1.22, over = kind == FFN_HIDDEN ? (big ? 30.0 : 10.0) : big ? 8.0 : 4.5;
         for (int s = 1; s <= 32; ++s) {
             if (s > 1 && (!may_split || s > steps / 4)) break;
             if (tiles * s > kMaxFfnTiles) break;
             double t = static_cast<double>(div_up(tiles * s, slots)) * (static_cast<double>(div_up(steps, s)) * step + over);
+            // float32 sums written and read, and a launch
             if (s > 1) t += 4.0 + static_cast<double>(count) * m * n * s * 8.0 / 4e6;
             if (t < least) {
                 least = t;
@@ -257,21 +267,24 @@ FfnPlan plan_ffn(int64_t m, int64_t n, int64_t steps, int count, bool may_split)
     return best;
 }
 
-constexpr int64_t kBkSteps = 64;
-FfnPlan plan_gated(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, 2 * x->hidden, div_up(x->width, kBkSteps), 1, false); }
-FfnPlan plan_down(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, x->width, div_up(x->hidden, kBkSteps), 1, true); }
-FfnPlan plan_hidden(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, x->hidden, div_up(x->width, kBkSteps), 1, false); }
-FfnPlan plan_input(const muon_feed_forward_args* x) { return plan_ffn(x->tokens, x->width, 2 * div_up(x->hidden, kBkSteps), 1, true); }
-FfnPlan plan_weights(const muon_feed_forward_args* x) { return plan_ffn(x->hidden, x->width, div_up(x->tokens, kBkSteps), 3, true); }
+FfnPlan plan_gated(const muon_feed_forward_args* x) { return plan_ffn(FFN_GATED, x->tokens, 2 * x->hidden, x->width, 1, 1, false); }
+FfnPlan plan_down(const muon_feed_forward_args* x) { return plan_ffn(FFN_PLAIN, x->tokens, x->width, x->hidden, 1, 1, true); }
+FfnPlan plan_hidden(const muon_feed_forward_args* x) { return plan_ffn(FFN_HIDDEN, x->tokens, x->hidden, x->width, 1, 1, false); }
+FfnPlan plan_input(const muon_feed_forward_args* x) { return plan_ffn(FFN_INPUT, x->tokens, x->width, x->hidden, 2, 1, true); }
+FfnPlan plan_weights(const muon_feed_forward_args* x) { return plan_ffn(FFN_WEIGHTS, x->hidden, x->width, x->tokens, 1, 3, true); }
 
 size_t part_bytes(const FfnPlan& p, int64_t m, int64_t n, int count) {
     return p.splits > 1 ? align256(static_cast<size_t>(p.splits) * m * n * sizeof(float)) * count : 0;
 }
 size_t hidden_bytes(const muon_feed_forward_args* x) { return align256(static_cast<size_t>(x->tokens) * x->hidden * 2); }
 
+// A few tokens of k values as whole fragments of 16 tokens by 32 values.
+size_t few_bytes(const muon_feed_forward_args* x, int64_t k) { return static_cast<size_t>(div_up(k, 32)) * div_up(x->tokens, 16) * 1024; }
 size_t forward_bytes(const muon_feed_forward_args* x) {
     // h, also where `kept` holds it: the size does not depend on the pointers
-    const size_t n = hidden_bytes(x) + part_bytes(plan_down(x), x->tokens, x->width, 1);
+    const size_t few = x->tokens <= kFewTokens ? few_bytes(x, x->hidden) + few_bytes(x, x->width) : 0;
+    size_t n = hidden_bytes(x) + part_bytes(plan_down(x), x->tokens, x->width, 1);
+    if (n < few) n = few;
     return n > 256 ? n : 256;
 }
 size_t backward_bytes(const muon_feed_forward_args* x) {
@@ -281,7 +294,7 @@ size_t backward_bytes(const muon_feed_forward_args* x) {
 }
 
 // One product of a launch; first: tiles of those before it.
-void add_seg(FfnGemm& g, int tile, bool gated, const bf16_t* p0, const bf16_t* p1, int64_t ldp, const bf16_t* q0,
+void add_seg(FfnGemm& g, FfnTile tile, bool gated, const bf16_t* p0, const bf16_t* p1, int64_t ldp, const bf16_t* q0,
              const bf16_t* q1, int64_t ldq, int64_t m, int64_t n, void* out, float* part) {
     FfnSeg& s = g.seg[g.nseg++];
     s.p[0] = p0;
@@ -302,7 +315,7 @@ void add_seg(FfnGemm& g, int tile, bool gated, const bf16_t* p0, const bf16_t* p
 void set_steps(FfnGemm& g, const FfnPlan& p, int64_t k, int phases) {
     g.k = k;
     g.phases = phases;
-    const int64_t steps = div_up(k, kBkSteps) * phases;
+    const int64_t steps = div_up(k, kFfnStep) * phases;
     g.split_steps = static_cast<int>(div_up(steps, p.splits));
     g.splits = p.splits;
     g.band = 8;
@@ -374,6 +387,28 @@ int muon_feed_forward(const muon_feed_forward_args* x, void* ws, size_t ws_bytes
     const int64_t t = x->tokens, h = x->hidden, w = x->width;
     const int64_t x_step = t > 1 ? x->x_stride : w;  // (of one row it may be anything)
     bf16_t* hid = x->kept ? x->kept + 2 * t * h : static_cast<bf16_t*>(ws);
+    if (!x->kept && t <= kFewTokens) {
+        FfnFew a{};
+        a.x = x->x;
+        a.w_gate = x->w_gate;
+        a.w_up = x->w_up;
+        a.w_down = x->w_down;
+        a.h = hid;
+        // x in fragments first where reading its rows in every workgroup costs more
+        // (1600 x 4264, 32 tokens: 32 us without, 31 with; 4096 x 10240, 32 tokens: 92 and
+        // 82, 16 tokens: 73 and 70, 8 tokens: 66 and 69)
+        if (static_cast<double>(t) * w * h >= 5e8) a.packed = hid + few_bytes(x, h) / 2;
+        a.out = x->out;
+        a.x_stride = x_step;
+        a.w_stride = x->w_stride;
+        a.w_down_stride = x->w_down_stride;
+        a.tokens = static_cast<int>(t);
+        a.width = static_cast<int>(w);
+        a.hidden = static_cast<int>(h);
+        a.act = static_cast<int>(x->activation);
+        const int st = launched(launch_ffn_few(a, s), "feed-forward block of a few tokens");
+        return st ? st : done();
+    }
     {
         const FfnPlan p = plan_gated(x);
         FfnGemm g{};

@@ -119,7 +119,19 @@ struct FfnGemm {
     int act;
     bf16_t *gate, *up, *dgate, *dup;  // FFN_GATED writes gate and up where given; FFN_HIDDEN reads them
 };
-// tile: 256 or 128 (square)
-hipError_t launch_ffn(FfnKind kind, int tile, const FfnGemm& g, hipStream_t stream);
+enum FfnTile { FFN_256 = 256, FFN_128 = 128 };  // output rows and columns of a workgroup
+constexpr int kFfnStep = 64;                    // K values of a step
+hipError_t launch_ffn(FfnKind kind, FfnTile tile, const FfnGemm& g, hipStream_t stream);
+
+// A few tokens, without what a backward pass needs (ffn_few.hip).
+constexpr int kFewTokens = 32;
+struct FfnFew {
+    const bf16_t *x, *w_gate, *w_up, *w_down;
+    bf16_t *h, *out;  // h: as fragments of 16 tokens by 32 values; out: contiguous
+    bf16_t* packed;   // x as such fragments, or null: read as it lies
+    int64_t x_stride, w_stride, w_down_stride;
+    int tokens, width, hidden, act;
+};
+hipError_t launch_ffn_few(const FfnFew& a, hipStream_t stream);
 
 }  // namespace muon
