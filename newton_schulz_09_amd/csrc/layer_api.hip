@@ -129,9 +129,9 @@ int run_resid(const muon_residual_norm_args* x, bool backward, void* ws, size_t 
     }
     if (full) row("gate", x->gate, yb, x->gate_stride);
     if (bad) return refuse(MUON_ERR_INVALID_ARG, "%s is null or not aligned to its type, or its stride is negative", bad);
-    if (x->gate_kind != GATE_NONE && !full && !x->gate) return refuse(MUON_ERR_INVALID_ARG, "gate is null");
-    if (backward && (x->gate_kind == GATE_CHANNEL || x->gate_kind == GATE_SEQUENCE) && !x->dgate)
-        return refuse(MUON_ERR_INVALID_ARG, "dgate is null");
+    const bool vector_gate = x->gate_kind == GATE_CHANNEL || (x->gate_kind == GATE_SEQUENCE && x->batch > 0);
+    if (vector_gate && !x->gate) return refuse(MUON_ERR_INVALID_ARG, "gate is null");
+    if (backward && vector_gate && !x->dgate) return refuse(MUON_ERR_INVALID_ARG, "dgate is null");
     if (backward && x->dresidual_scale && !x->residual_scale)
         return refuse(MUON_ERR_INVALID_ARG, "dresidual_scale without residual_scale");
     for (const void* p : {static_cast<const void*>(x->residual_scale), static_cast<const void*>(x->post_weight),
