@@ -270,7 +270,8 @@ typedef struct muon_feed_forward_args {
     int64_t dw_type;        /* muon_dtype */
 } muon_feed_forward_args;
 
-/* Bytes of workspace (at least 256; 0 for invalid sizes). */
+/* Bytes of workspace (at least 256; 0 for invalid sizes); of the forward pass
+ * for these args: it needs less where kept is given. */
 size_t muon_feed_forward_workspace_size(const muon_feed_forward_args *args);
 size_t muon_feed_forward_backward_workspace_size(const muon_feed_forward_args *args);
 

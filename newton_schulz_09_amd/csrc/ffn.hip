@@ -162,6 +162,74 @@ __device__ __forceinline__ void landed_but() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Segment, tile row and tile column of a launch's tile.
+__device__ __forceinline__ void locate(const FfnGemm& g, int tile, int& si, int& ti, int& tj) {
+    si = 0;
+#pragma unroll
+    for (int i = 1; i < 3; ++i)
+        if (i < g.nseg && tile >= g.seg[i].first) si = i;
+    const FfnSeg& seg = g.seg[si];
+    const int t = tile - seg.first, per_band = g.band * seg.tiles_n, band = t / per_band, first_row = band * g.band;
+    const int band_rows = seg.tiles_m - first_row < g.band ? seg.tiles_m - first_row : g.band;
+    const int in_band = t - band * per_band;
+    ti = first_row + in_band % band_rows;
+    tj = in_band / band_rows;
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+    reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ void add8(const float* p, float (&v)[8]) {
+    const f32x4 lo = reinterpret_cast<const f32x4*>(p)[0], hi = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] += lo[i];
+        v[4 + i] += hi[i];
+    }
+}
+
+// What becomes of 8 sums at element `at` of the output (`in`: inside it).
+__device__ __forceinline__ void finish_plain(const FfnGemm& g, const FfnSeg& seg, int64_t at, const float (&v)[8]) {
+    if (g.out_f32) store8(static_cast<float*>(seg.out) + at, v);
+    else *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(v);
+}
+__device__ __forceinline__ void finish_gated(const FfnGemm& g, const FfnSeg& seg, int64_t at, bool in, const float (&gt)[8],
+                                             const float (&up)[8]) {
+    float h[8];
+    by_act(g.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float v, unused;
+            activate<act>(gt[i], v, unused);
+            h[i] = v * up[i];
+        }
+    });
+    if (!in) return;
+    *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(h);
+    if (g.gate) {
+        *reinterpret_cast<u32x4*>(g.gate + at) = pack8(gt);
+        *reinterpret_cast<u32x4*>(g.up + at) = pack8(up);
+    }
+}
+__device__ __forceinline__ void finish_hidden(const FfnGemm& g, int64_t at, bool in, const float (&dh)[8], u32x4 gate, u32x4 up) {
+    float gt[8], u[8];
+    spread8(gate, gt);
+    spread8(up, u);
+    by_act(g.act, [&](auto act) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float v, dv;
+            activate<act>(gt[i], v, dv);
+            gt[i] = dh[i] * u[i] * dv;
+            u[i] = dh[i] * v;
+        }
+    });
+    if (!in) return;
+    *reinterpret_cast<u32x4*>(g.dgate + at) = pack8(gt);
+    *reinterpret_cast<u32x4*>(g.dup + at) = pack8(u);
+}
+
 template <int KIND, int BM, int BN, int WGM, int WGN, int BK>
 __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 2) void k_ffn(const FfnGemm g) {
     constexpr bool PT = KIND == FFN_WEIGHTS, QT = KIND == FFN_HIDDEN || KIND == FFN_INPUT || KIND == FFN_WEIGHTS;
@@ -177,17 +245,14 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
     const uint32_t lds = lds_addr(lds_mem);
 
     // ---- which split, segment and tile
-    const int place = xcd_place(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    const int split = place / g.tiles, tile = place - split * g.tiles;
-    int si = 0;
-#pragma unroll
-    for (int i = 1; i < 3; ++i)
-        if (i < g.nseg && tile >= g.seg[i].first) si = i;
+    // workgroups of whole tiles, then those of the tiles whose K is split
+    const int b = static_cast<int>(blockIdx.x), tail = g.tiles - g.full;
+    const bool whole = b < g.full;
+    const int place = whole ? xcd_place(b, g.full) : xcd_place(b - g.full, tail * g.splits);
+    const int split = whole ? 0 : place / tail, tile = whole ? place : g.full + place - split * tail;
+    int si, ti, tj;
+    locate(g, tile, si, ti, tj);
     const FfnSeg& seg = g.seg[si];
-    const int t = tile - seg.first, per_band = g.band * seg.tiles_n, band = t / per_band, first_row = band * g.band;
-    const int band_rows = seg.tiles_m - first_row < g.band ? seg.tiles_m - first_row : g.band;
-    const int in_band = t - band * per_band;
-    const int ti = first_row + in_band % band_rows, tj = in_band / band_rows;
     constexpr int BNO = GATED ? BN / 2 : BN;  // output columns of a tile
     const int64_t i0 = static_cast<int64_t>(ti) * BM, j0 = static_cast<int64_t>(tj) * BNO;
     const int lane = lane_id(), wave = attn::wave_id(), wm = wave / WGN, wn = wave % WGN;
@@ -203,7 +268,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
     const uint64_t q_next = KIND == FFN_INPUT || GATED ? q.base + (reinterpret_cast<uint64_t>(seg.q[1]) - reinterpret_cast<uint64_t>(seg.q[0])) : q.base;
 
     const int phase_steps = static_cast<int>((g.k + BK - 1) / BK), steps = phase_steps * g.phases;
-    const int s0 = split * g.split_steps, s1 = s0 + g.split_steps < steps ? s0 + g.split_steps : steps;
+    const int s0 = split * g.split_steps, s1 = !whole && s0 + g.split_steps < steps ? s0 + g.split_steps : steps;
     u32x4 dp, dq, dq_up;
     // Aims the loads at step s, the one after the step they were aimed at.  Most
     // steps move the descriptors on; the first and last ones of a product make
@@ -354,13 +419,14 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
     const uint32_t strip = lds + wave * STRIP;
     const int64_t row0 = i0 + wm * WTM, col = j0 + wn * COLS + 8 * (lane % LPR);
     typedef __attribute__((address_space(3))) f32x4* Chunk;
-    float* part = nullptr;
-    if constexpr (KIND >= FFN_INPUT || KIND == FFN_PLAIN)
-        part = seg.part ? seg.part + static_cast<int64_t>(split) * seg.m * seg.n : nullptr;
+    // of a split tile: its sums, as the tile lies (FFN_GATED: 32 columns of the gate
+    // and of the up projection in turn)
+    float* part = whole ? nullptr : g.part + (static_cast<int64_t>(split) * tail + (tile - g.full)) * (BM * BN) + wm * WTM * BN + wn * WTN;
     constexpr int TURNS = 32 / RPS;
     u32x4 gates[2][KIND == FFN_HIDDEN ? TURNS : 1][2];  // gate and up of this strip and the next, under way
     auto fetch = [&](auto m) {
-        if constexpr (KIND == FFN_HIDDEN && m < WTM / 32)
+        if constexpr (KIND == FFN_HIDDEN && m < WTM / 32) {
+            if (part) return;
             each<0, TURNS>([&](auto k) {
                 int64_t row = row0 + 32 * m + k * RPS + lane / LPR;
                 if (row >= seg.m) row = seg.m - 1;
@@ -368,6 +434,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
                 gates[m & 1][k][0] = *reinterpret_cast<const u32x4*>(g.gate + at);
                 gates[m & 1][k][1] = *reinterpret_cast<const u32x4*>(g.up + at);
             });
+        }
     };
     fetch(first);
     // every wave has read its last fragments (no load to LDS is under way)
@@ -393,97 +460,84 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
                     v[4 + i] = hi[i];
                 }
             };
-            const int64_t at = row * seg.n + col;
             const bool in = row < seg.m && col < seg.n;
+            float* to = part + (32 * m + r) * BN;
             if constexpr (GATED) {
                 // 32 columns of the gate, then the same 32 of the up projection
                 const int q8 = lane % LPR, c = q8 / 4 * 16 + q8 % 4 * 2;
-                float gt[8], up[8], h[8];
+                float gt[8], up[8];
                 take(c, gt);
                 take(c + 8, up);
-                by_act(g.act, [&](auto act) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float v, unused;
-                        activate<act>(gt[i], v, unused);
-                        h[i] = v * up[i];
+                if (part) {
+                    if (in) {
+                        store8(to + 4 * c, gt);
+                        store8(to + 4 * c + 32, up);
                     }
-                });
-                if (in) {
-                    *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(h);
-                    if (g.gate) {
-                        *reinterpret_cast<u32x4*>(g.gate + at) = pack8(gt);
-                        *reinterpret_cast<u32x4*>(g.up + at) = pack8(up);
-                    }
-                }
-            } else if constexpr (KIND == FFN_HIDDEN) {
-                float dh[8], gt[8], up[8];
-                take(2 * (lane % LPR), dh);
-                spread8(gates[m & 1][k][0], gt);
-                spread8(gates[m & 1][k][1], up);
-                by_act(g.act, [&](auto act) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float v, dv;
-                        activate<act>(gt[i], v, dv);
-                        gt[i] = dh[i] * up[i] * dv;
-                        up[i] = dh[i] * v;
-                    }
-                });
-                if (in) {
-                    *reinterpret_cast<u32x4*>(g.dgate + at) = pack8(gt);
-                    *reinterpret_cast<u32x4*>(g.dup + at) = pack8(up);
+                } else {
+                    finish_gated(g, seg, row * seg.n + col, in, gt, up);
                 }
             } else {
                 float v[8];
                 take(2 * (lane % LPR), v);
-                if (in) {
-                    if (part || g.out_f32) {
-                        float* o = (part ? part : static_cast<float*>(seg.out)) + at;
-                        reinterpret_cast<f32x4*>(o)[0] = f32x4{v[0], v[1], v[2], v[3]};
-                        reinterpret_cast<f32x4*>(o)[1] = f32x4{v[4], v[5], v[6], v[7]};
-                    } else {
-                        *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(v);
-                    }
+                if (part) {
+                    if (in) store8(to + 8 * (lane % LPR), v);
+                } else if constexpr (KIND == FFN_HIDDEN) {
+                    finish_hidden(g, row * seg.n + col, in, v, gates[m & 1][k][0], gates[m & 1][k][1]);
+                } else if (in) {
+                    finish_plain(g, seg, row * seg.n + col, v);
                 }
             }
         });
     });
 }
 
-// Sums of the splits, in their order: 8 values a thread.
+// The results of the split tiles, from their sums added in the splits' order: 8
+// columns a thread, a workgroup the BM BN / 2048 th part of a tile's columns.
+template <int KIND, int B>
 __global__ __launch_bounds__(256) void k_ffn_join(const FfnGemm g) {
-    const FfnSeg& seg = g.seg[blockIdx.y];
-    const int64_t n = static_cast<int64_t>(seg.m) * seg.n, at = 8 * (static_cast<int64_t>(block_place()) * 256 + threadIdx.x);
-    if (at >= n) return;
-    float v[8] = {};
-    for (int s = 0; s < g.splits; ++s) {
-        const f32x4* src = reinterpret_cast<const f32x4*>(seg.part + s * n + at);
-        const f32x4 lo = src[0], hi = src[1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] += lo[i];
-            v[4 + i] += hi[i];
-        }
+    constexpr bool GATED = KIND == FFN_GATED;
+    constexpr int BNO = GATED ? B / 2 : B, PER = B * BNO / 8 / 256;  // workgroups a tile
+    const int tail = g.tiles - g.full, tt = blockIdx.x / PER;
+    int si, ti, tj;
+    locate(g, g.full + tt, si, ti, tj);
+    const FfnSeg& seg = g.seg[si];
+    const int at = (blockIdx.x % PER) * 256 + threadIdx.x, r = at / (BNO / 8), o = at % (BNO / 8) * 8;
+    const int64_t row = static_cast<int64_t>(ti) * B + r, col = static_cast<int64_t>(tj) * BNO + o;
+    if (row >= seg.m || col >= seg.n) return;
+    const float* part = g.part + static_cast<int64_t>(tt) * (B * B) + r * B + (GATED ? o / 32 * 64 + o % 32 : o);
+    float v[8] = {}, up[8] = {};
+    for (int s = 0; s < g.splits; ++s, part += static_cast<int64_t>(tail) * (B * B)) {
+        add8(part, v);
+        if constexpr (GATED) add8(part + 32, up);
     }
-    if (g.out_f32) {
-        f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(seg.out) + at);
-        o[0] = f32x4{v[0], v[1], v[2], v[3]};
-        o[1] = f32x4{v[4], v[5], v[6], v[7]};
+    if constexpr (GATED) {
+        finish_gated(g, seg, row * seg.n + col, true, v, up);
+    } else if constexpr (KIND == FFN_HIDDEN) {
+        const int64_t to = row * seg.n + col;
+        finish_hidden(g, to, true, v, *reinterpret_cast<const u32x4*>(g.gate + to), *reinterpret_cast<const u32x4*>(g.up + to));
     } else {
-        *reinterpret_cast<u32x4*>(static_cast<bf16_t*>(seg.out) + at) = pack8(v);
+        finish_plain(g, seg, row * seg.n + col, v);
     }
+}
+
+template <int KIND, int B>
+void join(const FfnGemm& g, hipStream_t stream) {
+    constexpr int PER = B * (KIND == FFN_GATED ? B / 2 : B) / 8 / 256;
+    k_ffn_join<KIND, B><<<static_cast<uint32_t>(g.tiles - g.full) * PER, 256, 0, stream>>>(g);
 }
 
 template <int KIND>
 void start(FfnTile tile, const FfnGemm& g, hipStream_t stream) {
-    const uint32_t blocks = static_cast<uint32_t>(g.tiles) * g.splits;
+    const uint32_t blocks = static_cast<uint32_t>(g.full + (g.tiles - g.full) * g.splits);
     // The gated product's waves hold 64 rows by 128 columns, so that each writes
     // rows of 64 hidden values; the others' 128 by 64.  (GPT-2 124M batch: gated
     // 500 us against 540, gradients of the matrices 565 us and 552.)
     constexpr int WGM = KIND == FFN_GATED ? 4 : 2;
     if (tile == FFN_256) k_ffn<KIND, 256, 256, WGM, 8 / WGM, 64><<<blocks, 512, 0, stream>>>(g);
     else k_ffn<KIND, 128, 128, 2, 2, 64><<<blocks, 256, 0, stream>>>(g);
+    if (g.full == g.tiles) return;
+    if (tile == FFN_256) join<KIND, 256>(g, stream);
+    else join<KIND, 128>(g, stream);
 }
 
 }  // namespace
@@ -495,14 +549,6 @@ hipError_t launch_ffn(FfnKind kind, FfnTile tile, const FfnGemm& g, hipStream_t 
         case FFN_HIDDEN: start<FFN_HIDDEN>(tile, g, stream); break;
         case FFN_INPUT: start<FFN_INPUT>(tile, g, stream); break;
         case FFN_WEIGHTS: start<FFN_WEIGHTS>(tile, g, stream); break;
-    }
-    if (g.splits > 1) {
-        int64_t most = 0;
-        for (int i = 0; i < g.nseg; ++i) {
-            const int64_t n = static_cast<int64_t>(g.seg[i].m) * g.seg[i].n;
-            if (n > most) most = n;
-        }
-        k_ffn_join<<<long_grid((most / 8 + 255) / 256, 256, g.nseg), 256, 0, stream>>>(g);
     }
     return hipGetLastError();
 }

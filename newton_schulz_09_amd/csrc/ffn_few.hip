@@ -85,20 +85,8 @@ __device__ __forceinline__ void token_rows(const bf16_t* p, int64_t stride, int 
     }
 }
 
-// The tokens as the operand fragments in which the next kernel reads them, a
-// piece of 1 KB for 16 tokens by 32 values.
-template <int MT>
-__global__ __launch_bounds__(256) void k_few_pack(const FfnFew a) {
-    const int i = blockIdx.x * 256 + threadIdx.x, l = i & 63, m = i / 64 % MT, k = i / (64 * MT) * 32 + 8 * (l >> 4);
-    const int token = 16 * m + (l & 15);
-    if (k >= a.width) return;
-    u32x4 v = {0, 0, 0, 0};
-    if (token < a.tokens) v = *reinterpret_cast<const u32x4*>(a.x + token * a.x_stride + k);
-    reinterpret_cast<u32x4*>(a.packed)[i] = v;
-}
-
 // 16 hidden values a workgroup.
-template <int MT, int WAVES, bool PACKED>
+template <int MT, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_few_gated(const FfnFew a) {
     __shared__ f32x4 s[WAVES][2 * MT][64];
     const int lane = attn::lane_id(), wave = attn::wave_id();
@@ -107,14 +95,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_few_gated(const FfnFew a) {
     if (row >= a.hidden) row = a.hidden - 1;
     wp[0] = a.w_gate + row * a.w_stride;
     wp[1] = a.w_up + row * a.w_stride;
-    if constexpr (PACKED) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xp[m] = a.packed + (m * 64 + lane) * 8;
-    } else {
-        token_rows<MT>(a.x, a.x_stride, a.tokens, xp);
-    }
+    token_rows<MT>(a.x, a.x_stride, a.tokens, xp);
     f32x4 acc[2][MT];
-    stream<2, MT, WAVES, PACKED>(wp, xp, a.width, acc);
+    stream<2, MT, WAVES, false>(wp, xp, a.width, acc);
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -177,14 +160,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_few_down(const FfnFew a) {
 
 template <int MT>
 void start(const FfnFew& a, hipStream_t stream) {
-    const int grid = (a.hidden + 15) / 16;
-    if (a.packed) {
-        const int pieces = (a.width + 31) / 32 * MT * 64;
-        k_few_pack<MT><<<(pieces + 255) / 256, 256, 0, stream>>>(a);
-        k_few_gated<MT, 8, true><<<grid, 512, 0, stream>>>(a);
-    } else {
-        k_few_gated<MT, 8, false><<<grid, 512, 0, stream>>>(a);
-    }
+    k_few_gated<MT, 8><<<(a.hidden + 15) / 16, 512, 0, stream>>>(a);
     k_few_down<MT, 16><<<(a.width + 15) / 16, 1024, 0, stream>>>(a);
 }
 

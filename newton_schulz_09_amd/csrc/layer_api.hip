@@ -230,72 +230,91 @@ int check_matrix(const char* name, const void* p, int64_t rows, int64_t cols, in
 
 struct FfnPlan {
     FfnTile tile;
+    int64_t full;  // tiles computed whole; K of the others is split
     int splits;
+    size_t part;   // bytes of the splits' sums
 };
 
-// The tile and the number of splits of K that take the least time: rounds of
-// workgroups over the CUs times the steps of one, and the sums of the splits.
-// k: length of one product; phases: products summed.
+// The tile, the number of tiles that are computed whole and the number of splits
+// of the others' K that take the least time: rounds of workgroups over the CUs
+// times the steps of one.  Either whole rounds of tiles are computed whole and
+// the rest is split, so that the last round is no shorter than the others are
+// wide, or all tiles are split, or none.  k: length of one product; phases:
+// products summed; columns: of a tile, of the sums' and the output's.
 //
-// Measured on the products of a GPT-2 124M batch (65536 tokens, 768 to 2048), in
-// microseconds: a step of a 256 tile, one of which a CU holds, 1.9, of 128 tiles,
-// of which it holds two, 1.22; around the steps, where results are written, 8
-// and 4.5; where gate and up are read and their gradients written, 30 and 10.
-// (So the gradient of the hidden values takes 128 tiles, 396 us against 426, and
-// the others 256, gradients of the matrices 565 against 730.)
-FfnPlan plan_ffn(FfnKind kind, int64_t m, int64_t n, int64_t k, int phases, int count, bool may_split) {
-    FfnPlan best{FFN_128, 1};
+// The figures are fitted to the times of 572 plans of the five products at 11
+// sizes (64 to 8192 tokens, 768 to 4096 wide; off by 10% on average, and the plan
+// they choose is 1% slower than the fastest of those measured), in microseconds:
+// a step of a 256 tile, one of which a CU holds, 1.37; of 128 tiles 1.08 where a
+// CU holds two and 0.86 where it holds one; around the steps of a tile, where
+// results are written, `over`; the sums of splits 7, and 2.7 TB/s.
+FfnPlan plan_ffn(FfnKind kind, int64_t m, int64_t n, int64_t k, int phases, int count) {
+    FfnPlan best{};
     double least = 1e300;
     const int64_t steps = div_up(k, kFfnStep) * phases;
+    // gated, plain, hidden, input, weights
+    static const double over256[5] = {12.5, 2.5, 30.0, 5.5, 8.0}, over128[5] = {5.0, 0.0, 9.0, 0.5, 3.5};
     for (const FfnTile tile : {FFN_256, FFN_128}) {
         const bool big = tile == FFN_256;
-        const int64_t tiles = div_up(m, tile) * div_up(n, tile) * count, slots = big ? 256 : 512;
-        const double step = big ? 1.9 : 1.22, over = kind == FFN_HIDDEN ? (big ? 30.0 : 10.0) : big ? 8.0 : 4.5;
-        for (int s = 1; s <= 32; ++s) {
-            if (s > 1 && (!may_split || s > steps / 4)) break;
-            if (tiles * s > kMaxFfnTiles) break;
-            double t = static_cast<double>(div_up(tiles * s, slots)) * (static_cast<double>(div_up(steps, s)) * step + over);
-            // float32 sums written and read, and a launch
-            if (s > 1) t += 4.0 + static_cast<double>(count) * m * n * s * 8.0 / 4e6;
-            if (t < least) {
-                least = t;
-                best.tile = tile;
-                best.splits = s;
+        const int64_t tiles = div_up(m, tile) * div_up(n, kind == FFN_GATED ? tile / 2 : tile) * count, slots = big ? 256 : 512;
+        const double over = big ? over256[kind] : over128[kind];
+        // n workgroups of `steps` steps each, and `around` them
+        auto rounds = [&](int64_t n, int64_t steps, double around) {
+            const int64_t left = n % slots;
+            double t = static_cast<double>(n / slots) * (static_cast<double>(steps) * (big ? 1.37 : 1.08) + around);
+            if (left) t += static_cast<double>(steps) * (big ? 1.37 : left > 256 ? 1.08 : 0.86) + around;
+            return t;
+        };
+        for (const int64_t full : {tiles, tiles / slots * slots, int64_t{0}}) {
+            const int64_t tail = tiles - full;
+            for (int s = tail ? 2 : 1; s <= 32; ++s) {
+                if (s > 1 && (tail == 0 || s > steps / 2 || full + tail * s > kMaxFfnTiles)) break;
+                double t = rounds(full, steps, over);
+                if (tail) t += rounds(tail * s, div_up(steps, s), big ? 3.5 : 1.0) + 7.0 + static_cast<double>(tail) * tile * tile * s * 4.0 / 2.7e6;
+                if (t < least) {
+                    least = t;
+                    best.tile = tile;
+                    best.full = full;
+                    best.splits = s;
+                    best.part = align256(static_cast<size_t>(tail) * s * tile * tile * sizeof(float));
+                }
             }
         }
     }
     return best;
 }
 
-FfnPlan plan_gated(const muon_feed_forward_args* x) { return plan_ffn(FFN_GATED, x->tokens, 2 * x->hidden, x->width, 1, 1, false); }
-FfnPlan plan_down(const muon_feed_forward_args* x) { return plan_ffn(FFN_PLAIN, x->tokens, x->width, x->hidden, 1, 1, true); }
-FfnPlan plan_hidden(const muon_feed_forward_args* x) { return plan_ffn(FFN_HIDDEN, x->tokens, x->hidden, x->width, 1, 1, false); }
-FfnPlan plan_input(const muon_feed_forward_args* x) { return plan_ffn(FFN_INPUT, x->tokens, x->width, x->hidden, 2, 1, true); }
-FfnPlan plan_weights(const muon_feed_forward_args* x) { return plan_ffn(FFN_WEIGHTS, x->hidden, x->width, x->tokens, 1, 3, true); }
+FfnPlan plan_gated(const muon_feed_forward_args* x) { return plan_ffn(FFN_GATED, x->tokens, x->hidden, x->width, 1, 1); }
+FfnPlan plan_down(const muon_feed_forward_args* x) { return plan_ffn(FFN_PLAIN, x->tokens, x->width, x->hidden, 1, 1); }
+FfnPlan plan_hidden(const muon_feed_forward_args* x) { return plan_ffn(FFN_HIDDEN, x->tokens, x->hidden, x->width, 1, 1); }
+FfnPlan plan_input(const muon_feed_forward_args* x) { return plan_ffn(FFN_INPUT, x->tokens, x->width, x->hidden, 2, 1); }
+FfnPlan plan_weights(const muon_feed_forward_args* x) { return plan_ffn(FFN_WEIGHTS, x->hidden, x->width, x->tokens, 1, 3); }
 
-size_t part_bytes(const FfnPlan& p, int64_t m, int64_t n, int count) {
-    return p.splits > 1 ? align256(static_cast<size_t>(p.splits) * m * n * sizeof(float)) * count : 0;
-}
+size_t larger(size_t a, size_t b) { return a > b ? a : b; }
 size_t hidden_bytes(const muon_feed_forward_args* x) { return align256(static_cast<size_t>(x->tokens) * x->hidden * 2); }
 
-// A few tokens of k values as whole fragments of 16 tokens by 32 values.
-size_t few_bytes(const muon_feed_forward_args* x, int64_t k) { return static_cast<size_t>(div_up(k, 32)) * div_up(x->tokens, 16) * 1024; }
+// Whether the matrices are streamed past the tokens (ffn_few.hip) or tiles are
+// computed: 768 x 2048, 32 tokens 13 us and 23; 1600 x 4264, one token 23 and 28,
+// 16 tokens 26 and 29, 32 tokens 32 and 31; 4096 x 10240, one token 63 and 64, 8
+// tokens 66 and 64, 32 tokens 91 and 69.
+bool few_tokens(const muon_feed_forward_args* x) {
+    return !x->kept && x->tokens > 0 && x->tokens <= kFewTokens &&
+           static_cast<double>(x->tokens) * static_cast<double>(x->width) * static_cast<double>(x->hidden) < 2e8;
+}
+
 size_t forward_bytes(const muon_feed_forward_args* x) {
-    // h, also where `kept` holds it: the size does not depend on the pointers
-    const size_t few = x->tokens <= kFewTokens ? few_bytes(x, x->hidden) + few_bytes(x, x->width) : 0;
-    size_t n = hidden_bytes(x) + part_bytes(plan_down(x), x->tokens, x->width, 1);
-    if (n < few) n = few;
-    return n > 256 ? n : 256;
+    // few tokens: h as whole fragments of 16 tokens by 32 values
+    if (few_tokens(x)) return larger(static_cast<size_t>(div_up(x->hidden, 32)) * div_up(x->tokens, 16) * 1024, 256);
+    return larger((x->kept ? 0 : hidden_bytes(x)) + larger(plan_gated(x).part, plan_down(x).part), 256);
 }
 size_t backward_bytes(const muon_feed_forward_args* x) {
-    const size_t a = part_bytes(plan_input(x), x->tokens, x->width, 1), b = part_bytes(plan_weights(x), x->hidden, x->width, 3);
-    const size_t n = 2 * hidden_bytes(x) + (a > b ? a : b);
-    return n > 256 ? n : 256;
+    const size_t part = larger(plan_hidden(x).part, larger(plan_input(x).part, plan_weights(x).part));
+    return larger(2 * hidden_bytes(x) + part, 256);
 }
 
 // One product of a launch; first: tiles of those before it.
 void add_seg(FfnGemm& g, FfnTile tile, bool gated, const bf16_t* p0, const bf16_t* p1, int64_t ldp, const bf16_t* q0,
-             const bf16_t* q1, int64_t ldq, int64_t m, int64_t n, void* out, float* part) {
+             const bf16_t* q1, int64_t ldq, int64_t m, int64_t n, void* out) {
     FfnSeg& s = g.seg[g.nseg++];
     s.p[0] = p0;
     s.p[1] = p1;
@@ -309,15 +328,16 @@ void add_seg(FfnGemm& g, FfnTile tile, bool gated, const bf16_t* p0, const bf16_
     s.tiles_n = static_cast<int>(div_up(n, gated ? tile / 2 : tile));
     s.first = g.tiles;
     s.out = out;
-    s.part = part;
     g.tiles += s.tiles_m * s.tiles_n;
 }
-void set_steps(FfnGemm& g, const FfnPlan& p, int64_t k, int phases) {
+void set_steps(FfnGemm& g, const FfnPlan& p, int64_t k, int phases, float* part) {
     g.k = k;
     g.phases = phases;
+    g.full = p.full < g.tiles ? static_cast<int>(p.full) : g.tiles;
     const int64_t steps = div_up(k, kFfnStep) * phases;
-    g.split_steps = static_cast<int>(div_up(steps, p.splits));
     g.splits = p.splits;
+    g.split_steps = static_cast<int>(div_up(steps, p.splits));
+    g.part = g.full < g.tiles ? part : nullptr;
     g.band = 8;
 }
 
@@ -387,17 +407,13 @@ int muon_feed_forward(const muon_feed_forward_args* x, void* ws, size_t ws_bytes
     const int64_t t = x->tokens, h = x->hidden, w = x->width;
     const int64_t x_step = t > 1 ? x->x_stride : w;  // (of one row it may be anything)
     bf16_t* hid = x->kept ? x->kept + 2 * t * h : static_cast<bf16_t*>(ws);
-    if (!x->kept && t <= kFewTokens) {
+    if (few_tokens(x)) {
         FfnFew a{};
         a.x = x->x;
         a.w_gate = x->w_gate;
         a.w_up = x->w_up;
         a.w_down = x->w_down;
         a.h = hid;
-        // x in fragments first where reading its rows in every workgroup costs more
-        // (1600 x 4264, 32 tokens: 32 us without, 31 with; 4096 x 10240, 32 tokens: 92 and
-        // 82, 16 tokens: 73 and 70, 8 tokens: 66 and 69)
-        if (static_cast<double>(t) * w * h >= 5e8) a.packed = hid + few_bytes(x, h) / 2;
         a.out = x->out;
         a.x_stride = x_step;
         a.w_stride = x->w_stride;
@@ -409,11 +425,12 @@ int muon_feed_forward(const muon_feed_forward_args* x, void* ws, size_t ws_bytes
         const int st = launched(launch_ffn_few(a, s), "feed-forward block of a few tokens");
         return st ? st : done();
     }
+    float* part = reinterpret_cast<float*>(static_cast<char*>(ws) + (x->kept ? 0 : hidden_bytes(x)));
     {
         const FfnPlan p = plan_gated(x);
         FfnGemm g{};
-        add_seg(g, p.tile, true, x->x, nullptr, x_step, x->w_gate, x->w_up, x->w_stride, t, h, hid, nullptr);
-        set_steps(g, p, w, 1);
+        add_seg(g, p.tile, true, x->x, nullptr, x_step, x->w_gate, x->w_up, x->w_stride, t, h, hid);
+        set_steps(g, p, w, 1, part);
         g.act = static_cast<int>(x->activation);
         if (x->kept) {
             g.gate = x->kept;
@@ -424,9 +441,8 @@ int muon_feed_forward(const muon_feed_forward_args* x, void* ws, size_t ws_bytes
     {
         const FfnPlan p = plan_down(x);
         FfnGemm g{};
-        float* part = p.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(ws) + hidden_bytes(x)) : nullptr;
-        add_seg(g, p.tile, false, hid, nullptr, h, x->w_down, nullptr, x->w_down_stride, t, w, x->out, part);
-        set_steps(g, p, h, 1);
+        add_seg(g, p.tile, false, hid, nullptr, h, x->w_down, nullptr, x->w_down_stride, t, w, x->out);
+        set_steps(g, p, h, 1, part);
         if (int st = launched(launch_ffn(FFN_PLAIN, p.tile, g, s), "down projection")) return st;
     }
     return done();
@@ -458,8 +474,8 @@ int muon_feed_forward_backward(const muon_feed_forward_args* x, void* ws, size_t
     if (t > 0) {
         const FfnPlan p = plan_hidden(x);
         FfnGemm g{};
-        add_seg(g, p.tile, false, x->dout, nullptr, do_step, x->w_down, nullptr, x->w_down_stride, t, h, nullptr, nullptr);
-        set_steps(g, p, w, 1);
+        add_seg(g, p.tile, false, x->dout, nullptr, do_step, x->w_down, nullptr, x->w_down_stride, t, h, nullptr);
+        set_steps(g, p, w, 1, part);
         g.act = static_cast<int>(x->activation);
         g.gate = x->kept;
         g.up = x->kept + t * h;
@@ -470,19 +486,17 @@ int muon_feed_forward_backward(const muon_feed_forward_args* x, void* ws, size_t
     if (t > 0) {
         const FfnPlan p = plan_input(x);
         FfnGemm g{};
-        add_seg(g, p.tile, false, dgate, dup, h, x->w_gate, x->w_up, x->w_stride, t, w, x->dx, p.splits > 1 ? part : nullptr);
-        set_steps(g, p, h, 2);
+        add_seg(g, p.tile, false, dgate, dup, h, x->w_gate, x->w_up, x->w_stride, t, w, x->dx);
+        set_steps(g, p, h, 2, part);
         if (int st = launched(launch_ffn(FFN_INPUT, p.tile, g, s), "gradient of x")) return st;
     }
     {
         const FfnPlan p = plan_weights(x);
-        const size_t one = p.splits > 1 ? part_bytes(p, h, w, 1) / sizeof(float) : 0;
-        auto place = [&](int i) { return p.splits > 1 ? part + i * one : nullptr; };
         FfnGemm g{};
-        add_seg(g, p.tile, false, dgate, nullptr, h, x->x, nullptr, x_step, h, w, x->dw_gate, place(0));
-        add_seg(g, p.tile, false, dup, nullptr, h, x->x, nullptr, x_step, h, w, x->dw_up, place(1));
-        add_seg(g, p.tile, false, x->dout, nullptr, do_step, x->kept + 2 * t * h, nullptr, h, w, h, x->dw_down, place(2));
-        set_steps(g, p, t, 1);
+        add_seg(g, p.tile, false, dgate, nullptr, h, x->x, nullptr, x_step, h, w, x->dw_gate);
+        add_seg(g, p.tile, false, dup, nullptr, h, x->x, nullptr, x_step, h, w, x->dw_up);
+        add_seg(g, p.tile, false, x->dout, nullptr, do_step, x->kept + 2 * t * h, nullptr, h, w, h, x->dw_down);
+        set_steps(g, p, t, 1, part);
         g.out_f32 = x->dw_type == MUON_F32;
         if (int st = launched(launch_ffn(FFN_WEIGHTS, p.tile, g, s), "gradients of the matrices")) return st;
     }

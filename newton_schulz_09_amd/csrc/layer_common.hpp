@@ -106,14 +106,15 @@ struct FfnSeg {
     int m, n;
     int tiles_m, tiles_n, first;  // first: its first tile of the launch
     void* out;                    // m x n, contiguous
-    float* part;                  // [splits][m][n], or null where splits = 1
 };
 struct FfnGemm {
     FfnSeg seg[3];
     int nseg, tiles;         // tiles of all segments
     int64_t k;               // contracted length of one product
     int phases;              // products summed
-    int splits, split_steps; // K steps of a split
+    int full;                // the first `full` tiles are computed whole, K of the others is split
+    int splits, split_steps; // into so many parts of so many steps
+    float* part;             // [splits][tiles - full][tile][tile], or null where full = tiles
     int band;                // tile rows that go column by column together
     int out_f32;
     int act;
@@ -128,7 +129,6 @@ constexpr int kFewTokens = 32;
 struct FfnFew {
     const bf16_t *x, *w_gate, *w_up, *w_down;
     bf16_t *h, *out;  // h: as fragments of 16 tokens by 32 values; out: contiguous
-    bf16_t* packed;   // x as such fragments, or null: read as it lies
     int64_t x_stride, w_stride, w_down_stride;
     int tokens, width, hidden, act;
 };

@@ -516,11 +516,11 @@ def embedding_backward(dout, tokens, vocab, scale=1.0, dtype=None, out=None, wor
 
 def _rows(t, name):
     """The stride between the rows of the last dimension (any where there is at most one row)."""
+    if t.is_contiguous() and t.dim():
+        return t.shape[-1]
     if t.dim() == 0:
         raise ValueError(f"{name} must have a last dimension")
     _last(t, name)
-    if t.is_contiguous():
-        return t.shape[-1]
     step = count = None
     for n, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
@@ -628,6 +628,9 @@ def _resid_args(x, y, gate, scale, post_weight, pre_weight, post, eps, p, seed, 
 
 
 def _resid_types(x, y, dev, name):
+    if y is not None and isinstance(y, torch.Tensor) and x.dtype is _BF16 and y.dtype is _BF16 and x.is_cuda and y.device == dev \
+            and x.shape == y.shape and x.dim():
+        return
     _tensor(x, name, (_F32, _BF16), dev)
     if x.dim() < 1:
         raise ValueError(f"{name} must have a last dimension")
@@ -759,31 +762,31 @@ def residual_norm_backward(dz, dx_out, x_out, y=None, x=None, gate=None, residua
 
 
 def _matrix(t, name, dev, shape=None):
-    """bfloat16 rows on `dev`, one stride apart."""
-    _tensor(t, name, _BF16, dev, None if shape is None else len(shape))
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    """The stride between the rows of a bfloat16 tensor on `dev`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.is_cuda and t.device == dev
+            and (shape is None or t.shape == shape)):
+        _tensor(t, name, _BF16, dev, None if shape is None else len(shape))
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     return _rows(t, name)
 
 
-def _ffn_args(x, w_gate, w_up, w_down, activation, out, kept, dout, grads, dw_type, dev):
-    """The checked arguments as muon_feed_forward_args (None out, kept: none)."""
+def _ffn_sizes(x, w_gate, w_up, w_down, activation):
+    """Checks the forward pass's arguments: (device, (tokens, width, hidden), row strides of x, gate and up, down)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
     x_step = _matrix(x, "x", dev)
-    _tensor(w_gate, "w_gate", _BF16, dev, 2)
-    hidden, width = w_gate.shape
-    if x.shape[-1] != width:
-        raise ValueError(f"x {tuple(x.shape)} does not fit w_gate {tuple(w_gate.shape)}")
     w_step = _matrix(w_gate, "w_gate", dev)
-    if _matrix(w_up, "w_up", dev, (hidden, width)) != w_step:
+    if w_gate.dim() != 2 or x.shape[-1] != w_gate.shape[1]:
+        raise ValueError(f"x {tuple(x.shape)} does not fit w_gate {tuple(w_gate.shape)}")
+    hidden, width = w_gate.shape
+    if _matrix(w_up, "w_up", dev, w_gate.shape) != w_step:
         raise ValueError("the rows of w_gate and w_up must be the same stride apart")
     down_step = _matrix(w_down, "w_down", dev, (width, hidden))
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)} (got {activation!r})")
-    tokens = x.numel() // width if width else 0
-    a = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    return _FFN.pack(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), a(out), a(kept), a(dout),
-                     *[a(t) for t in grads], x_step, w_step, down_step, 0 if dout is None else _rows(dout, "dout"),
-                     tokens, width, hidden, ACTIVATIONS[activation], _DTYPE[dw_type])
+    return dev, (x.numel() // width if width else 0, width, hidden), (x_step, w_step, down_step)
 
 
 def feed_forward(x, w_gate, w_up, w_down, activation="silu", keep=False, out=None, workspace=None):
@@ -802,22 +805,16 @@ def feed_forward(x, w_gate, w_up, w_down, activation="silu", keep=False, out=Non
     stride (a multiple of 8) apart, the same for w_gate and w_up, so the halves
     of one matrix serve.  Sums are float32; the hidden values are rounded once.
     A given ``out`` must not share memory with anything."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    dev = x.device
-    _tensor(x, "x", _BF16, dev)
-    if x.dim() == 0:
-        raise ValueError("x must have a last dimension")
+    dev, sizes, steps = _ffn_sizes(x, w_gate, w_up, w_down, activation)
     given = out
     if out is None:
         out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _exactly(out, "out", _BF16, dev, x.shape)
-    kept = None
-    if keep:
-        _tensor(w_gate, "w_gate", _BF16, dev, 2)
-        kept = torch.empty((3, x.numel() // x.shape[-1] if x.shape[-1] else 0, w_gate.shape[0]), dtype=_BF16, device=dev)
-    args = _ffn_args(x, w_gate, w_up, w_down, activation, out, kept, None, (None,) * 4, _BF16, dev)
+    kept = torch.empty((3, sizes[0], sizes[2]), dtype=_BF16, device=dev) if keep else None
+    args = _FFN.pack(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), out.data_ptr(),
+                     kept.data_ptr() if keep else 0, 0, 0, 0, 0, 0, *steps, 0, *sizes, ACTIVATIONS[activation],
+                     muon.MUON_BF16)
     if given is not None:
         _apart(out, "out", (x, "x"), (w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))
     ptr, size, ws = _ws(workspace, _lib.muon_feed_forward_workspace_size(args) or 256, dev)
@@ -833,23 +830,19 @@ def feed_forward_backward(dout, x, w_gate, w_up, w_down, kept, activation="silu"
     as they are).  The gradients of the gate and of the up projection are
     rounded to bfloat16 once on the way.  A given ``dx`` must not share memory
     with anything."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    dev = x.device
-    _tensor(x, "x", _BF16, dev)
-    _matrix(dout, "dout", dev, x.shape)
+    dev, sizes, steps = _ffn_sizes(x, w_gate, w_up, w_down, activation)
+    dout_step = _matrix(dout, "dout", dev, x.shape)
     _float_type(dtype, "dtype")
-    for t, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
-        _tensor(t, name, _BF16, dev, 2)
-    width, hidden = x.shape[-1] if x.dim() else 0, w_gate.shape[0]
-    _exactly(kept, "kept", _BF16, dev, (3, x.numel() // width if width else 0, hidden))
+    _exactly(kept, "kept", _BF16, dev, (3, sizes[0], sizes[2]))
     given = dx
     if dx is None:
         dx = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _exactly(dx, "dx", _BF16, dev, x.shape)
     dws = [torch.empty(w.shape, dtype=dtype, device=dev) for w in (w_gate, w_up, w_down)]
-    args = _ffn_args(x, w_gate, w_up, w_down, activation, None, kept, dout, (dx, *dws), dtype, dev)
+    args = _FFN.pack(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr(), 0, kept.data_ptr(),
+                     dout.data_ptr(), dx.data_ptr(), *[t.data_ptr() for t in dws], *steps, dout_step, *sizes,
+                     ACTIVATIONS[activation], _DTYPE[dtype])
     if given is not None:
         _apart(dx, "dx", (dout, "dout"), (x, "x"), (w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"),
                (kept, "kept"))

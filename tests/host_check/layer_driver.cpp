@@ -102,17 +102,19 @@ hipError_t launch_ffn(FfnKind kind, FfnTile tile, const FfnGemm& g, hipStream_t)
         tiles += static_cast<int64_t>(s.tiles_m) * s.tiles_n;
         // offsets inside a tile stay below the one that means "past the end"
         if (s.ldp < 0 || s.ldq < 0 || wide{s.ldp} * 2 * 256 >= (wide{1} << 31) || wide{s.ldq} * 2 * 256 >= (wide{1} << 31)) die("strides", s.ldp, s.ldq);
-        if (g.splits > 1) apart(s.part, wide{g.splits} * s.m * s.n * 4, "sums of splits");
-        else if (s.part) die("parts without splits", i, 0);
         for (const bf16_t* p : {s.p[0], s.p[1], s.q[0]})
             if (p && is_ws(p)) in_ws(p, (kind == FFN_WEIGHTS ? wide{g.k} : wide{s.m}) * s.ldp * 2, "operand");
         if (s.out && is_ws(s.out)) in_ws(s.out, wide{s.m} * s.n * 2, "hidden values");
         if ((kind == FFN_HIDDEN) != (s.out == nullptr)) die("out", kind, 0);
     }
-    if (tiles != g.tiles || g.band < 1) die("tiles of all", tiles, g.tiles);
-    grid(wide{tiles} * g.splits, tile == FFN_256 ? 512 : 256, "feed-forward");
+    if (tiles != g.tiles || g.band < 1 || g.full < 0 || g.full > g.tiles) die("tiles of all", tiles, g.tiles);
+    const wide tail = g.tiles - g.full;
+    if (tail) apart(g.part, tail * g.splits * tile * tile * 4, "sums of splits");
+    else if (g.part) die("parts without splits", 0, 0);
+    grid(g.full + tail * g.splits, tile == FFN_256 ? 512 : 256, "feed-forward");
+    if (tail) grid(tail * tile * cols / 2048, 256, "join");
     const wide steps = (wide{g.k} + kFfnStep - 1) / kFfnStep * g.phases;
-    if (wide{g.splits} * g.split_steps < steps || steps > 0x7fffffff) die("steps", g.splits, g.split_steps);
+    if (g.splits < 1 || wide{g.splits} * g.split_steps < steps || steps > 0x7fffffff) die("steps", g.splits, g.split_steps);
     if (kind == FFN_HIDDEN)
         for (const bf16_t* p : {g.dgate, g.dup}) apart(p, wide{g.seg[0].m} * g.seg[0].n * 2, "gradients of gate and up");
     return hipSuccess;
@@ -123,7 +125,6 @@ hipError_t launch_ffn_few(const FfnFew& a, hipStream_t) {
     g_n = 0;
     const int m = a.tokens <= 16 ? 1 : 2;
     apart(a.h, (wide{a.hidden} + 31) / 32 * m * 1024, "hidden values in fragments");
-    if (a.packed) apart(a.packed, (wide{a.width} + 31) / 32 * m * 1024, "tokens in fragments");
     grid((a.hidden + 15) / 16, 512, "few, gated");
     grid((a.width + 15) / 16, 1024, "few, down");
     return hipSuccess;

