@@ -6,17 +6,23 @@
 //     dx = dgate Wg + dup Wu                              (one sum)
 //     dWg = dgate^T x, dWu = dup^T x, dWd = dout^T h      (one launch)
 //
-// Bound by the matrix cores for many tokens.  One engine: a workgroup computes
-// a BM x BN tile with WGM x WGN waves of 32 x 32 fragments; K advances 64 at a
-// time through two LDS stages that direct loads fill while the other is
-// multiplied, one barrier a step.  Operands contiguous along K lie in LDS as
-// rows of K and are read 16 bytes a lane; operands contiguous along the output
-// lie as rows of output and are read with transposing reads, so nothing is
-// ever transposed in memory.  Rows and columns past the matrices' ends come as
-// zeros from the loads' bounds checks, so every size runs the same loop.
+// Bound by the matrix cores, and on this card by the power they draw, for many
+// tokens.  One engine: a workgroup computes a 256 x 256 tile with 8 waves or a 128 x
+// 128 tile with 4, from 16 x 16 x 32 products, the form that draws least.  K
+// advances 64 at a time through LDS stages (three of P, two of Q) that direct
+// loads fill.  Operands contiguous along K lie in LDS as rows of K and are read
+// 16 bytes a lane; operands contiguous along the output lie as rows of output and
+// are read with transposing reads, so nothing is ever transposed in memory.  Rows
+// and columns past the matrices' ends come as zeros from the loads' bounds checks,
+// so every size runs the same loop.  The matrix instruction takes Q first, so a
+// lane holds 4 consecutive columns of one output row.
 //
-// The matrix instruction takes Q first, so a lane holds 4 consecutive columns
-// of one output row; two lanes swap halves and each stores 16 bytes.
+// Measured (averages; the first launches after a pause are a tenth faster): prefill of
+// 4001 tokens, 4096 to 10240: gate and up 646 us, down 305 (1.04 and 1.10 PFLOP/s; a
+// library's product of 8192^3 1.35).  GPT-2 124M batch, 65536 tokens, 768 to 2048:
+// gate and up 513 us (0.80 PFLOP/s: 12 steps a tile, then 805 MB of results), down 206
+// (1.0), gradients of the hidden values 408 (206 GFLOP, 1.2 GB), of x 396 (1.04), of
+// the matrices 573 and 24 for the sums over 7 splits (1.04).
 #include "../../include/muon.h"
 #include "ffn_common.hpp"
 
@@ -35,6 +41,7 @@ using attn::s16x4;
 using namespace ffn;
 
 constexpr int kXcds = 8;
+constexpr int BK = kFfnStep;
 constexpr uint32_t kOut = 0x80000000u;  // an offset past every buffer's end
 
 // Workgroup b of n -> place, so that each XCD (workgroups b = x, x + 8, ...)
@@ -44,23 +51,16 @@ __device__ __forceinline__ int xcd_place(int b, int n) {
     return x * q + (x < r ? x : r) + b / kXcds;
 }
 
-// Slot of 16-byte chunk c of row r is c ^ f(r).  Rows of K (8 or 4 chunks): 16
-// rows of one chunk fall on distinct banks.
-template <int CPR>
-__device__ __forceinline__ int rows_swizzle(int r) {
-    if constexpr (CPR == 8) return ((r >> 1) ^ (r << 2)) & 7;
-    else return ((r >> 1) ^ (r >> 3)) & 3;
-}
-// Rows of output (CPR chunks): the 8 rows that a transposing read touches (two
-// runs of 4, 8 apart) fall on distinct banks.
-template <int CPR>
-__device__ __forceinline__ int columns_swizzle(int r) {
-    return ((((r & 3) << 1) | ((r >> 3) & 1)) * (CPR >= 16 ? 2 : 1)) & (CPR - 1);
-}
+// Slot of 16-byte chunk c of row r is c ^ f(r).  Rows of K (8 chunks): 16 rows of
+// one chunk fall on distinct banks.
+__device__ __forceinline__ int rows_swizzle(int r) { return ((r >> 1) ^ (r << 2)) & 7; }
+// Rows of output (16 or 32 chunks): the 8 rows that half a transposing read
+// touches (two runs of 4, 8 apart) fall on distinct banks.
+__device__ __forceinline__ int columns_swizzle(int r) { return (((r & 3) << 1) | ((r >> 3) & 1)) * 2; }
 
 // One operand's tile: B output rows (or columns) by BK of K, COL: contiguous
 // along the output.  NW waves load it, N loads of 1 KB a wave.
-template <int B, int BK, bool COL, int NW>
+template <int B, bool COL, int NW>
 struct Operand {
     static constexpr int CPR = COL ? B / 8 : BK / 8;
     static constexpr int RPI = 64 / CPR;  // rows per load
@@ -76,7 +76,7 @@ struct Operand {
 
     __device__ __forceinline__ static int row_of(int wave, int i) { return (wave * N + i) * RPI + lane_id() / CPR; }
     __device__ __forceinline__ static int chunk_of(int row) {
-        return (lane_id() % CPR) ^ (COL ? columns_swizzle<CPR>(row) : rows_swizzle<CPR>(row));
+        return (lane_id() % CPR) ^ (COL ? columns_swizzle(row) : rows_swizzle(row));
     }
     // first: the tile's first output row; n: their number; place(row): the row's place from `first` on
     template <typename F>
@@ -127,7 +127,7 @@ struct Operand {
 
 // Fragments of 16 output rows, f of them from `row0` on, for the 32 K values of
 // slice kk: lane l holds row l % 16, K 8 (l / 16) .. + 7.
-template <int B, int BK, bool COL>
+template <int B, bool COL>
 struct Frags {
     uint32_t off;
     __device__ __forceinline__ void init(int row0) {
@@ -135,9 +135,9 @@ struct Frags {
         if constexpr (COL) {
             // transposing reads: lane r of 16 points at K r / 4 and 4 columns
             const int row = 8 * g + (r >> 2), col = row0 + 4 * (r & 3);
-            off = 2 * (row * B + (((col >> 3) ^ columns_swizzle<B / 8>(row)) << 3) + (col & 7));
+            off = 2 * (row * B + (((col >> 3) ^ columns_swizzle(row)) << 3) + (col & 7));
         } else {
-            off = 2 * ((row0 + r) * BK + ((g ^ rows_swizzle<BK / 8>(r)) << 3));
+            off = 2 * ((row0 + r) * BK + ((g ^ rows_swizzle(r)) << 3));
         }
     }
     // (the fragment's number, and of rows of K the slice's, are bits of the
@@ -169,8 +169,8 @@ __device__ __forceinline__ void locate(const FfnGemm& g, int tile, int& si, int&
     for (int i = 1; i < 3; ++i)
         if (i < g.nseg && tile >= g.seg[i].first) si = i;
     const FfnSeg& seg = g.seg[si];
-    const int t = tile - seg.first, per_band = g.band * seg.tiles_n, band = t / per_band, first_row = band * g.band;
-    const int band_rows = seg.tiles_m - first_row < g.band ? seg.tiles_m - first_row : g.band;
+    const int t = tile - seg.first, per_band = seg.band * seg.tiles_n, band = t / per_band, first_row = band * seg.band;
+    const int band_rows = seg.tiles_m - first_row < seg.band ? seg.tiles_m - first_row : seg.band;
     const int in_band = t - band * per_band;
     ti = first_row + in_band % band_rows;
     tj = in_band / band_rows;
@@ -230,22 +230,22 @@ __device__ __forceinline__ void finish_hidden(const FfnGemm& g, int64_t at, bool
     *reinterpret_cast<u32x4*>(g.dup + at) = pack8(u);
 }
 
-template <int KIND, int BM, int BN, int WGM, int WGN, int BK>
+template <int KIND, int BM, int BN, int WGM, int WGN>
 __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 2) void k_ffn(const FfnGemm g) {
     constexpr bool PT = KIND == FFN_WEIGHTS, QT = KIND == FFN_HIDDEN || KIND == FFN_INPUT || KIND == FFN_WEIGHTS;
     constexpr bool GATED = KIND == FFN_GATED;
     constexpr int NW = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 16, FN = WTN / 16;
     static_assert(!GATED || FN % 4 == 0, "a wave holds the gate and up columns of the same h");
-    using P = Operand<BM, BK, PT, NW>;
-    using Q = Operand<BN, BK, QT, NW>;
+    using P = Operand<BM, PT, NW>;
+    using Q = Operand<BN, QT, NW>;
     static_assert(!GATED || 32 % Q::RPI == 0, "a load takes rows of one matrix");
     constexpr int STRIP = 32 * WTN * 4, QAT = 3 * P::BYTES, LDS = QAT + 2 * Q::BYTES;
     static_assert(NW * STRIP <= LDS, "the results pass through the stages' memory");
     __shared__ __attribute__((aligned(1024))) char lds_mem[LDS];
     const uint32_t lds = lds_addr(lds_mem);
 
-    // ---- which split, segment and tile
-    // workgroups of whole tiles, then those of the tiles whose K is split
+    // ---- which split, segment and tile: workgroups of whole tiles, then those of
+    // the tiles whose K is split
     const int b = static_cast<int>(blockIdx.x), tail = g.tiles - g.full;
     const bool whole = b < g.full;
     const int place = whole ? xcd_place(b, g.full) : xcd_place(b - g.full, tail * g.splits);
@@ -302,8 +302,8 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
     };
     auto load_p = [&](int i, uint32_t to) { p.load(i, to, wave, dp); };
     auto load_q = [&](int i, uint32_t to) { q.load(i, to, wave, GATED && ((wave * Q::N + i) * Q::RPI / 32) & 1 ? dq_up : dq); };
-    Frags<BM, BK, PT> fp;
-    Frags<BN, BK, QT> fq;
+    Frags<BM, PT> fp;
+    Frags<BN, QT> fq;
     fp.init(wm * WTM);
     fq.init(wn * WTN);
 
@@ -533,8 +533,8 @@ void start(FfnTile tile, const FfnGemm& g, hipStream_t stream) {
     // rows of 64 hidden values; the others' 128 by 64.  (GPT-2 124M batch: gated
     // 500 us against 540, gradients of the matrices 565 us and 552.)
     constexpr int WGM = KIND == FFN_GATED ? 4 : 2;
-    if (tile == FFN_256) k_ffn<KIND, 256, 256, WGM, 8 / WGM, 64><<<blocks, 512, 0, stream>>>(g);
-    else k_ffn<KIND, 128, 128, 2, 2, 64><<<blocks, 256, 0, stream>>>(g);
+    if (tile == FFN_256) k_ffn<KIND, 256, 256, WGM, 8 / WGM><<<blocks, 512, 0, stream>>>(g);
+    else k_ffn<KIND, 128, 128, 2, 2><<<blocks, 256, 0, stream>>>(g);
     if (g.full == g.tiles) return;
     if (tile == FFN_256) join<KIND, 256>(g, stream);
     else join<KIND, 128>(g, stream);

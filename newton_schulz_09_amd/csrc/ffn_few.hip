@@ -6,7 +6,9 @@
 // values of K), with the tokens as the other operand, so a matrix is read once
 // and never passes through LDS.  K is split over the waves of a workgroup,
 // whose sums are joined through LDS in one order: 16 rows a workgroup keep the
-// whole chip reading also for small matrices.
+// whole chip reading also for small matrices.  Measured: one token of 768 to 2048
+// 4.7 and 4.7 us (9.4 MB; the time of a launch and one trip to memory), of 4096 to
+// 10240 63 us a call (252 MB, 4.0 TB/s).
 #include "../../include/muon.h"
 #include "ffn_common.hpp"
 

@@ -105,6 +105,7 @@ struct FfnSeg {
     int64_t ldp, ldq;
     int m, n;
     int tiles_m, tiles_n, first;  // first: its first tile of the launch
+    int band;                     // tile rows that go column by column together
     void* out;                    // m x n, contiguous
 };
 struct FfnGemm {
@@ -115,7 +116,6 @@ struct FfnGemm {
     int full;                // the first `full` tiles are computed whole, K of the others is split
     int splits, split_steps; // into so many parts of so many steps
     float* part;             // [splits][tiles - full][tile][tile], or null where full = tiles
-    int band;                // tile rows that go column by column together
     int out_f32;
     int act;
     bf16_t *gate, *up, *dgate, *dup;  // FFN_GATED writes gate and up where given; FFN_HIDDEN reads them

@@ -99,6 +99,7 @@ hipError_t launch_ffn(FfnKind kind, FfnTile tile, const FfnGemm& g, hipStream_t)
         const FfnSeg& s = g.seg[i];
         if (s.first != tiles) die("first tile", s.first, tiles);
         if (wide{s.tiles_m} * tile < s.m || wide{s.tiles_n} * cols < s.n || s.tiles_m < 1 || s.tiles_n < 1) die("tiles", s.m, s.n);
+        if (s.band < 1) die("band", s.band, 0);
         tiles += static_cast<int64_t>(s.tiles_m) * s.tiles_n;
         // offsets inside a tile stay below the one that means "past the end"
         if (s.ldp < 0 || s.ldq < 0 || wide{s.ldp} * 2 * 256 >= (wide{1} << 31) || wide{s.ldq} * 2 * 256 >= (wide{1} << 31)) die("strides", s.ldp, s.ldq);
@@ -107,7 +108,7 @@ hipError_t launch_ffn(FfnKind kind, FfnTile tile, const FfnGemm& g, hipStream_t)
         if (s.out && is_ws(s.out)) in_ws(s.out, wide{s.m} * s.n * 2, "hidden values");
         if ((kind == FFN_HIDDEN) != (s.out == nullptr)) die("out", kind, 0);
     }
-    if (tiles != g.tiles || g.band < 1 || g.full < 0 || g.full > g.tiles) die("tiles of all", tiles, g.tiles);
+    if (tiles != g.tiles || g.full < 0 || g.full > g.tiles) die("tiles of all", tiles, g.tiles);
     const wide tail = g.tiles - g.full;
     if (tail) apart(g.part, tail * g.splits * tile * tile * 4, "sums of splits");
     else if (g.part) die("parts without splits", 0, 0);
