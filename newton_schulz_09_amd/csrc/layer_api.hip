@@ -49,13 +49,15 @@ int check_resid(const muon_residual_norm_args* x) {
 }
 
 struct ResidPlan {
-    int waves, pieces, chunks, per;
+    int threads, pieces, chunks, per;
     int64_t blocks, groups;
     size_t off_gate, bytes;
 };
 
-// Waves that hold a row: 1 up to 1024 values, then as many as keep it at two
-// pieces of 8 a lane.
+// Threads that hold a row: a part of a wave that fits it up to 256 values, a wave
+// up to 1024, then as many as keep it at two pieces of 8 a thread.  (49728 rows of
+// 256 bf16, a wave and half a wave: 25 and 19 us, gradients 50 and 35; 65536 rows of
+// 100, a wave and 16 lanes: 57 and 20, gradients 152 and 49.)
 //
 // Backward, a workgroup leaves a row of up to 4 sums, which are written and read
 // again (as much as two rows of data): at most as many workgroups as the chip
@@ -63,18 +65,20 @@ struct ResidPlan {
 ResidPlan plan_resid(const muon_residual_norm_args* x, bool backward) {
     ResidPlan p{};
     const int64_t pieces = div_up(x->width, 8);
-    p.waves = pieces <= 128 ? 1 : pieces <= 256 ? 2 : pieces <= 512 ? 4 : 8;
+    const int64_t least = pieces <= 64 ? pieces : div_up(pieces, 2);
+    p.threads = 8;
+    while (p.threads < least) p.threads *= 2;
     p.pieces = pieces <= 64 ? 1 : 2;
-    const int64_t rows = x->batch * x->s, per_block = p.waves >= 4 ? 1 : 4 / p.waves;
+    const int64_t rows = x->batch * x->s, per_block = p.threads >= 256 ? 1 : 256 / p.threads;
     p.chunks = p.per = 1;
     p.groups = 1;
     if (!backward) {
-        const int64_t n = div_up(rows, per_block), most = p.waves == 8 ? 1024 : 2048;
+        const int64_t n = div_up(rows, per_block), most = p.threads == 512 ? 1024 : 2048;
         p.blocks = n < most ? n : most;
         p.bytes = 256;
         return p;
     }
-    const int64_t most = p.waves == 8 ? 256 : 512;
+    const int64_t most = p.threads == 512 ? 256 : 512;
     const bool by_sequence = x->gate_kind == GATE_SEQUENCE;
     p.groups = by_sequence ? x->batch : 1;
     const int64_t n = div_up(by_sequence ? x->s : rows, 4 * per_block);
@@ -183,7 +187,7 @@ int run_resid(const muon_residual_norm_args* x, bool backward, void* ws, size_t 
     a.gate_kind = static_cast<int>(x->gate_kind);
     a.post = x->post != 0;
     a.vector = vec;
-    a.waves = p.waves;
+    a.threads = p.threads;
     a.pieces = p.pieces;
     a.blocks = p.blocks;
     a.groups = p.groups;

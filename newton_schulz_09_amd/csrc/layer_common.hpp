@@ -74,7 +74,7 @@ struct ResidArgs {
     int x_type, y_type;     // muon_dtype of the stream and of the block
     int gate_kind, post;
     int vector;             // rows of aligned pieces of 8
-    int waves, pieces;      // waves that hold a row, pieces a lane
+    int threads, pieces;    // threads that hold a row, pieces a thread
     int64_t blocks;
     // backward: groups of rows share a gate (GATE_SEQUENCE: a sequence each); a
     // group is split into `chunks` workgroups, or a workgroup takes `per` groups

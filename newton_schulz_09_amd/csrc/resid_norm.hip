@@ -9,7 +9,7 @@
 //     dprew = sum dz v r'.
 //
 // Bound by memory: every row is read once and written once and stays in
-// registers between.  W waves hold a row, 8 values a piece and 2 pieces a lane,
+// registers between.  T threads hold a row, 8 values a piece and 1 or 2 pieces each,
 // so a row of 1024 values needs no exchange but that inside its wave.
 // Workgroups walk rows, so weights are loaded and gradients of weights summed
 // in registers; a second, small kernel joins the workgroups' sums in one order.
@@ -111,31 +111,36 @@ template <int CTRL>
 __device__ __forceinline__ float dpp_add(float x) {
     return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
 }
-// Sum over the wave, in every lane.
-__device__ __forceinline__ float wave_sum(float x) {
+// Sum over groups of T lanes (at most 64), in every lane.
+template <int T>
+__device__ __forceinline__ float lanes_sum(float x) {
     x = dpp_add<0xB1>(x);   // lanes 1 0 3 2
     x = dpp_add<0x4E>(x);   // lanes 2 3 0 1
     x = dpp_add<0x141>(x);  // 8 lanes mirrored
+    if constexpr (T == 8) return x;
     x = dpp_add<0x140>(x);  // 16 lanes mirrored
+    if constexpr (T == 16) return x;
     auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    if constexpr (T == 32) return x;
     r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-template <int W>
-constexpr int threads_of() { return 64 * (W > 4 ? W : 4); }
+// Threads of a workgroup whose rows have T threads each.
+template <int T>
+constexpr int threads_of() { return T > 256 ? T : 256; }
 
-// Sums of K values over the W waves of each row, in every lane of the row.
-template <int W>
+// Sums of K values over the T threads of each row, in every lane of the row.
+template <int T>
 struct RowSum {
-    static constexpr int ROWS = threads_of<W>() / 64 / W;
+    static constexpr int ROWS = threads_of<T>() / T, W = T > 64 ? T / 64 : 1;
     float (*s)[ROWS][W][4];
     int flip = 0;
     template <int K>
     __device__ __forceinline__ void operator()(float (&x)[K]) {
 #pragma unroll
-        for (int k = 0; k < K; ++k) x[k] = wave_sum(x[k]);
+        for (int k = 0; k < K; ++k) x[k] = lanes_sum<(T < 64 ? T : 64)>(x[k]);
         if constexpr (W > 1) {
             // two buffers in turn: a barrier lies between a buffer's reads and its next writes
             const int wave = threadIdx.x >> 6, row = wave / W;
@@ -184,12 +189,12 @@ struct Dropper {
     }
 };
 
-template <typename TX, typename TY, int NP, int W, bool ALIGNED>
-__global__ __launch_bounds__(threads_of<W>()) void k_resid_norm(const ResidArgs a) {
-    constexpr int ROWS = threads_of<W>() / 64 / W;
-    __shared__ float s_sum[2][ROWS][W][4];
-    RowSum<W> row_sum{s_sum};
-    const int l = threadIdx.x % (64 * W), sub = threadIdx.x / (64 * W);
+template <typename TX, typename TY, int NP, int T, bool ALIGNED>
+__global__ __launch_bounds__(threads_of<T>()) void k_resid_norm(const ResidArgs a) {
+    constexpr int ROWS = threads_of<T>() / T;
+    __shared__ float s_sum[2][ROWS][RowSum<T>::W][4];
+    RowSum<T> row_sum{s_sum};
+    const int l = threadIdx.x % T, sub = threadIdx.x / T;
     const float inv = 1.0f / static_cast<float>(a.width);
     uint64_t seed = 0, first = 0;
     if (a.drop.threshold) drop_start(a.drop, seed, first);
@@ -197,7 +202,7 @@ __global__ __launch_bounds__(threads_of<W>()) void k_resid_norm(const ResidArgs 
     int left[NP];  // values of the row from the piece on
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-        const int c = (p * 64 * W + l) * V;
+        const int c = (p * T + l) * V;
         left[p] = a.width - c;
         load_weights<ALIGNED>(a.postw, c, left[p], postw[p]);
         load_weights<ALIGNED>(a.prew, c, left[p], prew[p]);
@@ -211,7 +216,7 @@ __global__ __launch_bounds__(threads_of<W>()) void k_resid_norm(const ResidArgs 
         Raw<TY, ALIGNED> ry[NP], rg[NP];
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int c = (p * 64 * W + l) * V;
+            const int c = (p * T + l) * V;
             rx[p].zero();
             ry[p].zero();
             rg[p].zero();
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(threads_of<W>()) void k_resid_norm(const ResidArgs 
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                const int c = (p * 64 * W + l) * V;
+                const int c = (p * T + l) * V;
                 const float mine = left[p] > 0 ? r : 0.0f;  // (r is infinite for a row of zeros without eps)
                 float n[V];
 #pragma unroll
@@ -272,7 +277,7 @@ __global__ __launch_bounds__(threads_of<W>()) void k_resid_norm(const ResidArgs 
         sum[0] = 0.0f;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int c = (p * 64 * W + l) * V;
+            const int c = (p * T + l) * V;
             if (real && left[p] > 0 && a.x_out) store_piece<TX, ALIGNED>(static_cast<TX*>(a.x_out) + row * a.width + c, v[p], left[p]);
 #pragma unroll
             for (int i = 0; i < V; ++i) sum[0] = fmaf(v[p][i], v[p][i], sum[0]);
@@ -281,7 +286,7 @@ __global__ __launch_bounds__(threads_of<W>()) void k_resid_norm(const ResidArgs 
         const float r = 1.0f / sqrtf(fmaf(sum[0], inv, a.eps));
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int c = (p * 64 * W + l) * V;
+            const int c = (p * T + l) * V;
             float z[V];
 #pragma unroll
             for (int i = 0; i < V; ++i) z[i] = v[p][i] * r * prew[p][i];
@@ -292,14 +297,14 @@ __global__ __launch_bounds__(threads_of<W>()) void k_resid_norm(const ResidArgs 
 
 // Sum of every row of the workgroup, column by column: the waves that hold the
 // same columns are added in one order.  s: ROWS x width.
-template <int NP, int W>
+template <int NP, int T>
 __device__ __forceinline__ void sum_rows(const float (&x)[NP][V], float* s, float* dst, int width) {
-    constexpr int ROWS = threads_of<W>() / 64 / W;
-    const int l = threadIdx.x % (64 * W), sub = threadIdx.x / (64 * W);
+    constexpr int ROWS = threads_of<T>() / T;
+    const int l = threadIdx.x % T, sub = threadIdx.x / T;
     if constexpr (ROWS == 1) {
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int c = (p * 64 * W + l) * V;
+            const int c = (p * T + l) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (c + i < width) dst[c + i] = x[p][i];
@@ -308,13 +313,13 @@ __device__ __forceinline__ void sum_rows(const float (&x)[NP][V], float* s, floa
         __syncthreads();
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-            const int c = (p * 64 * W + l) * V;
+            const int c = (p * T + l) * V;
 #pragma unroll
             for (int i = 0; i < V; ++i)
                 if (c + i < width) s[sub * width + c + i] = x[p][i];
         }
         __syncthreads();
-        for (int c = threadIdx.x; c < width; c += threads_of<W>()) {
+        for (int c = threadIdx.x; c < width; c += threads_of<T>()) {
             float t = s[c];
 #pragma unroll
             for (int r = 1; r < ROWS; ++r) t += s[r * width + c];
@@ -326,13 +331,13 @@ __device__ __forceinline__ void sum_rows(const float (&x)[NP][V], float* s, floa
 // Backward the vectors lie in LDS, 4 values of a lane side by side with the
 // next lane's: with them in registers beside the sums of their gradients fewer
 // waves fit.
-template <typename TX, typename TY, int NP, int W, bool ALIGNED>
-__global__ __launch_bounds__(threads_of<W>(), 2) void k_resid_norm_bwd(const ResidArgs a) {
-    constexpr int ROWS = threads_of<W>() / 64 / W, T = 64 * W;
-    __shared__ float s_sum[2][ROWS][W][4];
+template <typename TX, typename TY, int NP, int T, bool ALIGNED>
+__global__ __launch_bounds__(threads_of<T>(), 2) void k_resid_norm_bwd(const ResidArgs a) {
+    constexpr int ROWS = threads_of<T>() / T;
+    __shared__ float s_sum[2][ROWS][RowSum<T>::W][4];
     __shared__ float s_col[ROWS > 1 ? ROWS * T * NP * V : 1];
     __shared__ f32x4 s_w[4][NP * 2 * T];  // prew, scale, gate, postw
-    RowSum<W> row_sum{s_sum};
+    RowSum<T> row_sum{s_sum};
     const int l = threadIdx.x % T, sub = threadIdx.x / T;
     const float inv = 1.0f / static_cast<float>(a.width);
     uint64_t seed = 0, first = 0;
@@ -518,15 +523,15 @@ __global__ __launch_bounds__(threads_of<W>(), 2) void k_resid_norm_bwd(const Res
                     store_piece<TY, ALIGNED>(static_cast<TY*>(a.dy) + row * a.width + (p * T + l) * V, u[p], left[p]);
         }
         if (by_sequence)
-            sum_rows<NP, W>(dgate, s_col,
+            sum_rows<NP, T>(dgate, s_col,
                             a.gate_part ? a.gate_part + (g * a.chunks + chunk) * a.width : static_cast<float*>(a.dgate) + g * a.width,
                             a.width);
     }
     float* part = a.part + static_cast<int64_t>(blockIdx.x) * 4 * a.width;
-    if (a.dprew) sum_rows<NP, W>(dpre, s_col, part, a.width);
-    if (a.dpostw) sum_rows<NP, W>(dpost, s_col, part + a.width, a.width);
-    if (a.dscale) sum_rows<NP, W>(dscale, s_col, part + 2 * a.width, a.width);
-    if (a.dgate && a.gate_kind == GATE_CHANNEL) sum_rows<NP, W>(dgate, s_col, part + 3 * a.width, a.width);
+    if (a.dprew) sum_rows<NP, T>(dpre, s_col, part, a.width);
+    if (a.dpostw) sum_rows<NP, T>(dpost, s_col, part + a.width, a.width);
+    if (a.dscale) sum_rows<NP, T>(dscale, s_col, part + 2 * a.width, a.width);
+    if (a.dgate && a.gate_kind == GATE_CHANNEL) sum_rows<NP, T>(dgate, s_col, part + 3 * a.width, a.width);
 }
 
 // Sums of the workgroups' rows: blockIdx.y < 4 of the vectors, and from 4 on of
@@ -565,20 +570,24 @@ __global__ __launch_bounds__(1024) void k_resid_join(const ResidArgs a) {
     if (y == 0 && c < a.width) dst[c] = s[0][threadIdx.x & 15];
 }
 
-template <typename TX, typename TY, int NP, int W, bool ALIGNED>
+template <typename TX, typename TY, int NP, int T, bool ALIGNED>
 void start(const ResidArgs& a, bool backward, hipStream_t stream) {
     const uint32_t blocks = static_cast<uint32_t>(a.blocks);
-    if (backward) k_resid_norm_bwd<TX, TY, NP, W, ALIGNED><<<blocks, threads_of<W>(), 0, stream>>>(a);
-    else k_resid_norm<TX, TY, NP, W, ALIGNED><<<blocks, threads_of<W>(), 0, stream>>>(a);
+    if (backward) k_resid_norm_bwd<TX, TY, NP, T, ALIGNED><<<blocks, threads_of<T>(), 0, stream>>>(a);
+    else k_resid_norm<TX, TY, NP, T, ALIGNED><<<blocks, threads_of<T>(), 0, stream>>>(a);
 }
 
 template <typename TX, typename TY, bool ALIGNED>
 void by_width(const ResidArgs& a, bool backward, hipStream_t stream) {
-    if (a.waves == 1 && a.pieces == 1) start<TX, TY, 1, 1, ALIGNED>(a, backward, stream);
-    else if (a.waves == 1) start<TX, TY, 2, 1, ALIGNED>(a, backward, stream);
-    else if (a.waves == 2) start<TX, TY, 2, 2, ALIGNED>(a, backward, stream);
-    else if (a.waves == 4) start<TX, TY, 2, 4, ALIGNED>(a, backward, stream);
-    else start<TX, TY, 2, 8, ALIGNED>(a, backward, stream);
+    switch (a.threads) {
+        case 8: return start<TX, TY, 1, 8, ALIGNED>(a, backward, stream);
+        case 16: return start<TX, TY, 1, 16, ALIGNED>(a, backward, stream);
+        case 32: return start<TX, TY, 1, 32, ALIGNED>(a, backward, stream);
+        case 64: return a.pieces == 1 ? start<TX, TY, 1, 64, ALIGNED>(a, backward, stream) : start<TX, TY, 2, 64, ALIGNED>(a, backward, stream);
+        case 128: return start<TX, TY, 2, 128, ALIGNED>(a, backward, stream);
+        case 256: return start<TX, TY, 2, 256, ALIGNED>(a, backward, stream);
+        default: return start<TX, TY, 2, 512, ALIGNED>(a, backward, stream);
+    }
 }
 
 template <typename TX, typename TY>

@@ -66,20 +66,20 @@ hipError_t launch_dropout(const DropArgs& a, hipStream_t) {
 }
 
 static void rows_of(const ResidArgs& a) {
-    if (static_cast<int64_t>(a.waves) * a.pieces * 64 * 8 < a.width) die("a row does not fit its waves", a.waves, a.width);
-    if ((a.waves != 1 && a.waves != 2 && a.waves != 4 && a.waves != 8) || a.pieces < 1 || a.pieces > 2 ||
-        (a.pieces == 1 && a.waves != 1))
-        die("no kernel", a.waves, a.pieces);
+    if (static_cast<int64_t>(a.threads) * a.pieces * 8 < a.width) die("a row does not fit its threads", a.threads, a.width);
+    if (a.threads < 8 || a.threads > 512 || (a.threads & (a.threads - 1)) || a.pieces < 1 || a.pieces > 2 ||
+        (a.pieces == 1 ? a.threads > 64 : a.threads < 64))
+        die("no kernel", a.threads, a.pieces);
 }
 hipError_t launch_resid_norm(const ResidArgs& a, hipStream_t) {
     rows_of(a);
-    grid(a.blocks, a.waves == 8 ? 512 : 256, "norms");
+    grid(a.blocks, a.threads == 512 ? 512 : 256, "norms");
     return hipSuccess;
 }
 hipError_t launch_resid_norm_bwd(const ResidArgs& a, hipStream_t) {
     rows_of(a);
     g_n = 0;
-    if (a.blocks > 0) grid(a.blocks, a.waves == 8 ? 512 : 256, "norms backward");
+    if (a.blocks > 0) grid(a.blocks, a.threads == 512 ? 512 : 256, "norms backward");
     apart(a.part, wide{a.blocks} * 4 * a.width * 4, "sums of vectors");
     if (a.gate_part) apart(a.gate_part, wide{a.groups} * a.chunks * a.width * 4, "sums of gates");
     if (a.chunks < 1 || a.per < 1 || (a.chunks > 1 && a.per > 1)) die("chunks", a.chunks, a.per);

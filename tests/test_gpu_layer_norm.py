@@ -84,6 +84,14 @@ def test_numbers_of_rows(lm, b, s, gate):
     run(lm, b, s, 72, F, F, gate=gate, scale=True)
 
 
+# rows that share a wave: 8, 16 and 32 lanes each, and more rows than a turn of the workgroups takes
+@pytest.mark.parametrize("width", [63, 64, 65, 120, 128, 129, 249, 256, 264])
+@pytest.mark.parametrize("stream,block", [(B, B), (F, B)])
+@pytest.mark.parametrize("b,s,gate", [(1, 1, "channel"), (3, 33, "sequence"), (2, 31, "full"), (5, 211, "sequence"), (1, 997, "channel")])
+def test_narrow_rows(lm, b, s, gate, stream, block, width):
+    run(lm, b, s, width, stream, block, gate=gate, scale=True, p=0.25)
+
+
 @pytest.mark.parametrize("stream,block", [(B, B), (F, B), (F, F)])
 @pytest.mark.parametrize("width", [96, 99, 2048])
 def test_without_a_block(lm, stream, block, width):
