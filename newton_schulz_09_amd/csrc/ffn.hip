@@ -230,8 +230,11 @@ __device__ __forceinline__ void finish_hidden(const FfnGemm& g, int64_t at, bool
     *reinterpret_cast<u32x4*>(g.dup + at) = pack8(u);
 }
 
-template <int KIND, int BM, int BN, int WGM, int WGN>
-__global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 2) void k_ffn(const FfnGemm g) {
+// ONE: K is one step (gradients of the matrices from up to 64 tokens), so the operands
+// have a stage each and four workgroups fit a CU: 36 tokens of 3056 to 11600, 213 MB of
+// gradients, 66 us with two workgroups and 50 with four.
+template <int KIND, int BM, int BN, int WGM, int WGN, bool ONE = false>
+__global__ __launch_bounds__(64 * WGM * WGN, ONE ? 4 : BM * BN / (WGM * WGN) > 8192 ? 1 : 2) void k_ffn(const FfnGemm g) {
     constexpr bool PT = KIND == FFN_WEIGHTS, QT = KIND == FFN_HIDDEN || KIND == FFN_INPUT || KIND == FFN_WEIGHTS;
     constexpr bool GATED = KIND == FFN_GATED;
     constexpr int NW = WGM * WGN, WTM = BM / WGM, WTN = BN / WGN, FM = WTM / 16, FN = WTN / 16;
@@ -239,7 +242,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
     using P = Operand<BM, PT, NW>;
     using Q = Operand<BN, QT, NW>;
     static_assert(!GATED || 32 % Q::RPI == 0, "a load takes rows of one matrix");
-    constexpr int STRIP = 32 * WTN * 4, QAT = 3 * P::BYTES, LDS = QAT + 2 * Q::BYTES;
+    constexpr int STRIP = 32 * WTN * 4, QAT = (ONE ? 1 : 3) * P::BYTES, LDS = QAT + (ONE ? 1 : 2) * Q::BYTES;
     static_assert(NW * STRIP <= LDS, "the results pass through the stages' memory");
     __shared__ __attribute__((aligned(1024))) char lds_mem[LDS];
     const uint32_t lds = lds_addr(lds_mem);
@@ -341,7 +344,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
         each<0, P::N>([&](auto i) { load_p(i, lds); });
         aim_q(s0);
         each<0, Q::N>([&](auto i) { load_q(i, lds + QAT); });
-        if (s0 + 1 < s1) {
+        if (!ONE && s0 + 1 < s1) {
             aim_p(s0 + 1);
             each<0, P::N>([&](auto i) { load_p(i, lds + P::BYTES); });
             aim_q(s0 + 1);
@@ -356,7 +359,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, BM * BN / (WGM * WGN) > 8192 ? 1 : 
     uint32_t p_here = lds, p_there = lds + P::BYTES, p_third = lds + 2 * P::BYTES;
     uint32_t q_here = lds + QAT, q_there = lds + QAT + Q::BYTES;
     for (int s = s0; s < s1; ++s) {
-        const bool more = s + 1 < s1, more2 = s + 2 < s1;
+        const bool more = !ONE && s + 1 < s1, more2 = !ONE && s + 2 < s1;
         in_order();
         if (more2) aim_p(s + 2);
         each<0, 2>([&](auto kk) {
@@ -533,6 +536,10 @@ void start(FfnTile tile, const FfnGemm& g, hipStream_t stream) {
     // rows of 64 hidden values; the others' 128 by 64.  (GPT-2 124M batch: gated
     // 500 us against 540, gradients of the matrices 565 us and 552.)
     constexpr int WGM = KIND == FFN_GATED ? 4 : 2;
+    if (KIND == FFN_WEIGHTS && tile == FFN_128 && g.k <= BK) {
+        k_ffn<FFN_WEIGHTS, 128, 128, 2, 2, true><<<blocks, 256, 0, stream>>>(g);
+        return;
+    }
     if (tile == FFN_256) k_ffn<KIND, 256, 256, WGM, 8 / WGM><<<blocks, 512, 0, stream>>>(g);
     else k_ffn<KIND, 128, 128, 2, 2><<<blocks, 256, 0, stream>>>(g);
     if (g.full == g.tiles) return;

@@ -256,6 +256,12 @@ FfnPlan plan_ffn(FfnKind kind, int64_t m, int64_t n, int64_t k, int phases, int 
     FfnPlan best{};
     double least = 1e300;
     const int64_t steps = div_up(k, kFfnStep) * phases;
+    if (kind == FFN_WEIGHTS && steps <= 1) {  // the kernel of one step; nothing to split
+        best.tile = FFN_128;
+        best.full = div_up(m, FFN_128) * div_up(n, FFN_128) * count;
+        best.splits = 1;
+        return best;
+    }
     // gated, plain, hidden, input, weights
     static const double over256[5] = {12.5, 2.5, 30.0, 5.5, 8.0}, over128[5] = {5.0, 0.0, 9.0, 0.5, 3.5};
     for (const FfnTile tile : {FFN_256, FFN_128}) {
