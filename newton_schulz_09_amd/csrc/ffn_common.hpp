@@ -58,7 +58,8 @@ __device__ __forceinline__ void activate(float g, float& a, float& da) {
         // (1 + tanh v) / 2 = sigmoid(2 v)
         const float s = sigmoid(1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.0f));
         a = g * s;
-        da = fmaf(a * (1.0f - s), 1.5957691216057308f * fmaf(0.134145f * g, g, 1.0f), s);
+        // (the slope of v is infinite from |g| = 5e19 on, where 1 - s or a is zero)
+        da = fmaf(a * (1.0f - s), 1.5957691216057308f * fminf(fmaf(0.134145f * g, g, 1.0f), 1e38f), s);
     } else {
         a = g < 0.0f ? 0.0f : g;
         da = g > 0.0f ? 1.0f : 0.0f;

@@ -84,3 +84,14 @@ def test_tails(lm, name, n):
     few, h, dg, du = run(lm, g, name, n)
     for got, want, what in ((few, a, "out"), (h, a, "h"), (du, a, "du"), (dg, da, "dg")):
         relative(got, want, g, (name, n, what))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_large_gates(lm, name):
+    """Finite gates of any size."""
+    g = torch.tensor([2.0 ** e for e in (5, 10, 20, 40, 60, 62, 63, 64, 65, 66, 70, 80, 100, 120, 126, 127)], dtype=torch.float64).to(B)
+    g = torch.cat([g, -g])
+    few, h, dg, du = run(lm, g, name, 3)
+    a, da = definition(name, g)
+    for got, want, what in ((few, a, "out"), (h, a, "h"), (du, a, "du"), (dg, da, "dg")):
+        relative(got, want, g, (name, what))
