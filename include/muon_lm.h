@@ -202,7 +202,9 @@ typedef enum { MUON_GATE_NONE = 0, MUON_GATE_CHANNEL = 1, MUON_GATE_SEQUENCE = 2
  * that the forward pass returned: dx, dy and the gradients of gate,
  * residual_scale and the weights; sums over rows are float32 in one order.
  * Given NULL, weights and residual_scale are ones and have no gradient; a
- * weight's gradient is not computed where its pointer is NULL.
+ * weight's gradient is not computed where its pointer is NULL.  A row whose dz
+ * and dx_out are zeros adds nothing to them if it is finite in x, y and x_out
+ * (and, where eps is 0, not all zeros in y or x_out).
  */
 typedef struct muon_residual_norm_args {
     const void *x;        /* [batch s][width] of stream_type; backward: read for dresidual_scale only */
@@ -283,7 +285,8 @@ size_t muon_feed_forward_backward_workspace_size(const muon_feed_forward_args *a
  * MUON_ERR_WORKSPACE.
  */
 int muon_feed_forward(const muon_feed_forward_args *args, void *workspace, size_t workspace_bytes, void *stream);
-/* dx, dw_gate, dw_up and dw_down; no tokens give zeros for the matrices. */
+/* dx, dw_gate, dw_up and dw_down; no tokens give zeros for the matrices.  A
+ * token whose dout is zero adds nothing to them if it is finite in x and kept. */
 int muon_feed_forward_backward(const muon_feed_forward_args *args, void *workspace, size_t workspace_bytes,
                                void *stream);
 

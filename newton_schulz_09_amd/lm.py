@@ -711,8 +711,10 @@ def residual_norm_backward(dz, dx_out, x_out, y=None, x=None, gate=None, residua
     of its results, its result ``x_out`` and its arguments; None for what was
     not given.  ``x`` is needed with a residual_scale only.  dx has x_out's
     type, dy and dz y's (without y dz is float32 or bfloat16), dgate is as gate,
-    the others are float32; sums over rows are float32, in one order.  A given
-    ``dx`` may be dx_out, and a given ``dy`` dz or y, where those are
+    the others are float32; sums over rows are float32, in one order.  A row of a
+    padded batch whose dz and dx_out are zeros adds nothing to them if it is
+    finite in x, y and x_out (and, with an eps of 0, not all zeros there).  A
+    given ``dx`` may be dx_out, and a given ``dy`` dz or y, where those are
     contiguous; else they must not share memory with anything."""
     if not isinstance(x_out, torch.Tensor):
         raise TypeError("x_out must be a torch.Tensor")
@@ -828,8 +830,9 @@ def feed_forward_backward(dout, x, w_gate, w_up, w_down, kept, activation="silu"
     ``dout``, its arguments and what it kept.  dx is bfloat16; the matrices'
     gradients are contiguous and of ``dtype`` (bfloat16, or float32: their sums
     as they are).  The gradients of the gate and of the up projection are
-    rounded to bfloat16 once on the way.  A given ``dx`` must not share memory
-    with anything."""
+    rounded to bfloat16 once on the way.  A token of a padded batch whose dout is
+    zero adds nothing to the matrices' gradients if it is finite in x and kept.
+    A given ``dx`` must not share memory with anything."""
     dev, sizes, steps = _ffn_sizes(x, w_gate, w_up, w_down, activation)
     dout_step = _matrix(dout, "dout", dev, x.shape)
     _float_type(dtype, "dtype")
