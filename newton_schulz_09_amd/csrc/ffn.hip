@@ -17,12 +17,13 @@
 // so every size runs the same loop.  The matrix instruction takes Q first, so a
 // lane holds 4 consecutive columns of one output row.
 //
-// Measured (averages; the first launches after a pause are a tenth faster): prefill of
-// 4001 tokens, 4096 to 10240: gate and up 646 us, down 305 (1.04 and 1.10 PFLOP/s; a
-// library's product of 8192^3 1.35).  GPT-2 124M batch, 65536 tokens, 768 to 2048:
-// gate and up 513 us (0.80 PFLOP/s: 12 steps a tile, then 805 MB of results), down 206
-// (1.0), gradients of the hidden values 408 (206 GFLOP, 1.2 GB), of x 396 (1.04), of
-// the matrices 573 and 24 for the sums over 7 splits (1.04).
+// Measured (averages of 12 calls; after a pause the third to tenth take up to 40% longer
+// than those from the thirtieth on): prefill of
+// 4001 tokens, 4096 to 10240: gate and up 623 us, down 293 (1.08 and 1.15 PFLOP/s; a
+// library's product of 8192^3 1.1 to 1.4).  GPT-2 124M batch, 65536 tokens, 768 to 2048:
+// gate and up 515 us (0.80 PFLOP/s: 12 steps a tile, then 805 MB of results), down 205
+// (1.0), gradients of the hidden values 410 (206 GFLOP, 1.1 GB), of x 398 (1.04), of
+// the matrices 588 and 24 for the sums over 7 splits (1.01).
 #include "../../include/muon.h"
 #include "ffn_common.hpp"
 

@@ -5,10 +5,12 @@
 // straight into the matrix cores' operand registers (lane l: row l % 16, 8
 // values of K), with the tokens as the other operand, so a matrix is read once
 // and never passes through LDS.  K is split over the waves of a workgroup,
-// whose sums are joined through LDS in one order: 16 rows a workgroup keep the
-// whole chip reading also for small matrices.  Measured: one token of 768 to 2048
-// 4.7 and 4.7 us (9.4 MB; the time of a launch and one trip to memory), of 4096 to
-// 10240 63 us a call (252 MB, 4.0 TB/s).
+// whose sums are joined through LDS in one order: 16 rows a workgroup, hidden / 16
+// workgroups for h and width / 16 for the result.  The latter are fewer than the
+// 256 CUs below a width of 4096 (48 at 768, 100 at 1600), which then read less
+// than memory gives.  Measured: one token of 768 to 2048 4.5 and 4.5 us (9.4 MB; the
+// time of a launch and one trip to memory), of 1600 to 4264 23 us a call (41 MB, 1.8
+// TB/s), of 4096 to 10240 63 (252 MB, 4.0 TB/s).
 #include "../../include/muon.h"
 #include "ffn_common.hpp"
 

@@ -80,7 +80,7 @@ struct ResidArgs {
     // group is split into `chunks` workgroups, or a workgroup takes `per` groups
     int64_t groups;
     int chunks, per;
-    float* part;            // [blocks][3][width]: sums for prew, postw, scale
+    float* part;            // [blocks][4][width]: sums for prew, postw, scale, gate (GATE_CHANNEL)
     float* gate_part;       // [groups][chunks][width], or null where chunks = 1
     float eps;
     DropState drop;         // threshold 0: none

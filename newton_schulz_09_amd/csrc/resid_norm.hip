@@ -14,10 +14,10 @@
 // Workgroups walk rows, so weights are loaded and gradients of weights summed
 // in registers; a second, small kernel joins the workgroups' sums in one order.
 // Measured, forward: 65536 rows of 768 bf16 76 us (403 MB, 5.3 TB/s).  Gradients: the
-// same with dropout and four vectors' gradients 153 us and 5 for the join (4.6 TB/s),
-// 8192 rows of 2048 with a gate each element 51 us (5.3), 2331 of 1600 with a float32
-// stream 26 us (2.5: under five rows a workgroup, whose loads wait for the sums of the
-// row before).
+// same with dropout and four vectors' gradients 155 us and 5 for the join (4.5 TB/s),
+// 8192 rows of 2048 with a gate each element 49 us (5.4), 2331 of 1600 with a float32
+// stream 26 us (2.5: 294 workgroups with eight rows each, two at a time, whose loads
+// wait for the sums of the rows before).
 #include <type_traits>
 
 #include "../../include/muon.h"
